@@ -7,9 +7,10 @@ CUDA device, and raises otherwise.
 
 Functions take torch tensors and pass their device pointers:
     canvas_attn, unembed, linear, sample_commit, unembed_sample_commit, kv_block_commit,
-    canvas_attn_e4m3, quantize_e4m3, linear_e4m3, unembed_e4m3, unembed_sample_commit_e4m3,
-    philox
+    canvas_attn_e4m3, kv_append_e4m3, paged_attn_e4m3, quantize_e4m3, linear_e4m3, unembed_e4m3, unembed_sample_commit_e4m3,
+    philox, rope_table
 Objects:
+    PagedCache  codes and scales of a paged e4m3 KV cache (one layer)
     DgModel   weights + configuration (dg_model)
     DgState   KV caches and canvas state of a batch (dg_state)
     prefill, denoise_logits, denoise_block
@@ -24,7 +25,8 @@ from ._lib import (EPI_BF16, EPI_F32, EPI_GELU_BF16, EPI_RESID_F32, MASK_BIDIR, 
 
 __all__ = ["canvas_attn", "canvas_attn_e4m3", "unembed", "linear", "sample_commit", "unembed_sample_commit",
            "quantize_e4m3", "linear_e4m3", "unembed_e4m3", "unembed_sample_commit_e4m3",
-           "kv_block_commit", "philox",
+           "kv_block_commit", "kv_append_e4m3", "paged_attn_e4m3", "PagedCache", "rope_table",
+           "philox",
            "DgModel", "DgState", "SamplerSettings", "prefill", "denoise_logits", "denoise_block",
            "linear_plan_of", "model_residual_on_pairs", "set_wait_limit_ns", "self_test_wait",
            "check_device_errors", "Workspace", "DgError", "MASK_BIDIR", "MASK_CAUSAL",
@@ -293,6 +295,132 @@ def kv_block_commit(k_blk, v_blk, k_cache, v_cache, cache_len, *, n_kv_heads, he
     vc = arr(*[t.data_ptr() for t in v_cache])
     _lib.check(_lib.load().dg_kv_block_commit(kb, vb, ld, kc, vc, _ptr(cache_len), n, B,
                                               n_kv_heads, C, head_dim, lmax, _stream(stream)))
+
+
+class PagedCache:
+    """One layer's paged e4m3 KV cache: k_pages, v_pages uint8 [n_pages, Hkv, page, hd] (e4m3
+    codes) and k_exp, v_exp uint8 [n_pages, Hkv] (a page's scale is 2^(exp - 127))."""
+
+    def __init__(self, k_pages, v_pages, k_exp, v_exp):
+        for t in (k_pages, v_pages, k_exp, v_exp):
+            if t.dtype != torch.uint8:
+                raise ValueError("codes and exponents must be uint8")
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or \
+                k_exp.shape != k_pages.shape[:2] or v_exp.shape != k_exp.shape:
+            raise ValueError("pages must be [n_pages, Hkv, page, hd], exponents [n_pages, Hkv]")
+        _need_contig(k_pages, v_pages, k_exp, v_exp)
+        self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
+
+    @classmethod
+    def zeros(cls, n_pages, n_kv_heads, page, head_dim, device="cuda"):
+        shape = (n_pages, n_kv_heads, page, head_dim)
+        return cls(*[torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)],
+                   *[torch.full(shape[:2], 127, dtype=torch.uint8, device=device)
+                     for _ in range(2)])
+
+
+def rope_table(n_positions, rot_dim, base=10000.0, device="cuda"):
+    """Angles of positions 0..n_positions-1 for kv_append_e4m3: fp32 [n_positions, rot_dim / 2, 2],
+    the cos and sin of position * base^(-2 i / rot_dim), formed in fp64 and rounded once."""
+    half = rot_dim // 2
+    freq = base ** (-torch.arange(half, device=device, dtype=torch.float64) / half)
+    angle = torch.arange(n_positions, device=device, dtype=torch.float64)[:, None] * freq
+    return torch.stack([angle.cos(), angle.sin()], -1).float().contiguous()
+
+
+def _rows(t, name, dtype=torch.bfloat16):
+    """Row stride of a packed [T, ld] tensor."""
+    if t.dtype != dtype or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be [T, ld] {dtype} with unit inner stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _paged_batch(cache, page_table, tok_start, cache_len, others):
+    """Checks of the index tensors that append and attention share."""
+    for t in (page_table, tok_start, cache_len):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("page_table, tok_start and cache_len must be contiguous int32")
+    B = cache_len.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != B or tok_start.shape != (B + 1,):
+        raise ValueError("page_table must be [B, max_pages], tok_start [B + 1], cache_len [B]")
+    dev = torch.cuda.current_device()
+    for t in (cache.k_pages, cache.v_pages, cache.k_exp, cache.v_exp, page_table, tok_start,
+              cache_len, *others):
+        if t is not None and t.device.index != dev:
+            raise ValueError("every tensor must be on the current CUDA device")
+    return B
+
+
+def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, rope=None,
+                   interleaved=False, q=None, q_out=None, stream=None):
+    """Rotate new keys (and queries) by their positions; store keys and values in the pages.
+
+    k, v [T, Hkv*hd] bf16 (views allowed via their row stride); cache a PagedCache;
+    page_table [B, max_pages], tok_start [B + 1], cache_len [B] int32 (device); max_new a bound
+    on every sequence's new rows; rope [n, rot_dim / 2, 2] fp32 (rope_table) or None; q, q_out
+    [T, Hq*hd] bf16, the queries and where their rotated values go (q_out may be q).
+    """
+    n_pages, Hkv, page, hd = cache.k_pages.shape
+    B = _paged_batch(cache, page_table, tok_start, cache_len, (k, v, rope, q, q_out))
+    ldkv = _rows(k, "k")
+    T = k.shape[0]
+    if T == 0:
+        return
+    if v.shape[0] != T or _rows(v, "v") != ldkv or k.shape[1] < Hkv * hd or v.shape[1] < Hkv * hd:
+        raise ValueError("k and v must be [T, >= Hkv*hd] and share a row stride")
+    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or
+                             rope.shape[2] != 2 or not rope.is_contiguous()):
+        raise ValueError("rope must be contiguous fp32 [positions, rot_dim / 2, 2]")
+    Hq = ldq = ldqo = 0
+    if q is not None and q_out is not None:
+        Hq = q.shape[1] // hd
+        ldq, ldqo = _rows(q, "q"), _rows(q_out, "q_out")
+        if q.shape[0] != T or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [T, Hq*hd]")
+    _lib.check(_lib.load().dg_kv_append_e4m3(
+        _ptr(k), _ptr(v), ldkv, _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(rope),
+        rope.shape[0] if rope is not None else 0, 2 * rope.shape[1] if rope is not None else 0,
+        1 if interleaved else 0, _ptr(cache.k_pages), _ptr(cache.v_pages), _ptr(cache.k_exp),
+        _ptr(cache.v_exp), n_pages, page, _ptr(page_table), page_table.shape[1], _ptr(tok_start),
+        _ptr(cache_len), max_new, B, T, Hkv, hd, _stream(stream)))
+
+
+def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_prefix, out, *,
+                    n_q_heads, lse=None, scale=None, mask=MASK_BIDIR, ws=None, stream=None):
+    """Attention of the packed new rows over everything cached of their sequence.
+
+    q, out [T, >=Hq*hd] bf16 (views allowed via their row stride); lse [T, Hq] fp32 or None;
+    cache, page_table, tok_start, cache_len and max_new as in kv_append_e4m3, which stored the
+    rows' own keys; max_prefix a bound on every cache_len.  ws: a Workspace of the caller's for
+    this stream or graph; without one the call takes its scratch from torch's allocator.
+    """
+    n_pages, Hkv, page, hd = cache.k_pages.shape
+    B = _paged_batch(cache, page_table, tok_start, cache_len, (q, out, lse))
+    ldq, ldo = _rows(q, "q"), _rows(out, "out")
+    T = q.shape[0]
+    if T == 0:
+        return out
+    if out.shape[0] != T or q.shape[1] < n_q_heads * hd or out.shape[1] < n_q_heads * hd:
+        raise ValueError("q and out must be [T, >= Hq*hd]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, n_q_heads) or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [T, Hq]")
+    lib = _lib.load()
+    need = lib.dg_paged_attn_workspace_bytes(B, T, n_q_heads, Hkv, hd, max_new, max_prefix)
+    wp, wn = None, 0
+    if need and ws is not None:
+        wp, wn = ws.args(need)
+    elif need:
+        s = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(s):
+            buf = torch.empty(need, dtype=torch.uint8, device=q.device)
+        wp, wn = _ptr(buf), need
+    _lib.check(lib.dg_paged_attn_e4m3(
+        _ptr(q), ldq, _ptr(cache.k_pages), _ptr(cache.v_pages), _ptr(cache.k_exp),
+        _ptr(cache.v_exp), n_pages, page, _ptr(page_table), page_table.shape[1], _ptr(tok_start),
+        _ptr(cache_len), max_new, max_prefix, _ptr(out), ldo, _ptr(lse), B, T, n_q_heads, Hkv, hd,
+        hd ** -0.5 if scale is None else scale, mask, wp, wn, _stream(stream)))
+    return out
 
 
 def philox(inp, out, stream=None):

@@ -84,6 +84,15 @@ SIGNATURES = {
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
                                     c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int,
                                     c_int, c_float, c_int, c_void_p, c_size_t, c_void_p]),
+    "dg_kv_append_e4m3": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p, c_int,
+                                  c_int, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p,
+                                  c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    "dg_paged_attn_e4m3": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                   c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                                   c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                   c_float, c_int, c_void_p, c_size_t, c_void_p]),
+    "dg_paged_attn_workspace_bytes": (c_size_t, [c_int] * 7),
     "dg_unembed": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_size_t,
                            c_void_p]),
     "dg_linear": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p,

@@ -20,8 +20,10 @@
 #include "attn.cuh"
 #include "dg_common.cuh"
 #include "gemm.cuh"
+#include "kvappend.cuh"
 #include "kvcommit.cuh"
 #include "norm.cuh"
+#include "paged_attn.cuh"
 #include "quant.cuh"
 #include "unembed.cuh"
 #include "sampler.cuh"
@@ -179,6 +181,28 @@ int make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
   if (r != CUDA_SUCCESS)
     return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled (u8) failed (%d) inner=%llu rows=%llu",
                 (int)r, (unsigned long long)inner, (unsigned long long)rows);
+  return DG_OK;
+}
+
+// The codes of a paged cache's K or V: rows of hd bytes, box = one page of one
+// kv head.  K lands swizzled (rows of 128 or 64 bytes: an operand tile), V plain.
+int make_tmap_pages(CUtensorMap* m, const void* base, int hd, uint64_t rows, int page,
+                    bool swizzled) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)hd, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)hd};
+  cuuint32_t box[2] = {(cuuint32_t)hd, (cuuint32_t)page};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapSwizzle sw = !swizzled   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                            : CU_TENSOR_MAP_SWIZZLE_64B;
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled (pages) failed (%d) hd=%d rows=%llu page=%d",
+                (int)r, hd, (unsigned long long)rows, page);
   return DG_OK;
 }
 
@@ -630,6 +654,91 @@ int launch_attn_e4m3(const uint8_t* q, int ldq, const float* q_scale, const uint
     DG_CUDA(launch_ex(dg::attn::attn_combine_kernel<128>, dim3(cdiv(rows * 32, threads)),
                       dim3(threads), 0, s, 1, (const __nv_bfloat16*)p.part_o,
                       (const float*)p.part_lse, S, B, Hq, Lq, (__nv_bfloat16*)out, ldo, lse));
+    count_launch();
+    DG_CUDA(cudaGetLastError());
+  }
+  return DG_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Paged e4m3 KV cache
+// ---------------------------------------------------------------------------
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// Sizes that every paged call checks: positions and cache rows stay in int range.
+int check_paged(const char* fn, int n_pages, int page, int max_pages, int B, int T, int Hkv, int hd,
+                int max_new) {
+  if (n_pages < 1 || max_pages < 1 || B < 1 || B > 65535 || T < 0 || Hkv < 1 || max_new < 0)
+    return fail(DG_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (hd != 64 && hd != 128)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: head_dim %d not in {64,128}", fn, hd);
+  if (!page_ok(page))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: page %d not in {16,32,64,128}", fn, page);
+  const long long most = 0x7FFFFFFFll - 256;
+  if ((long long)n_pages * page > most / Hkv || (long long)max_pages * page > most)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^31 cache rows or positions", fn);
+  return DG_OK;
+}
+
+template <int HD>
+int launch_append(const dg::paged::AppendParams& p, int blocks, cudaStream_t s) {
+  DG_CUDA(launch_ex(dg::paged::append_kernel<HD>, dim3(blocks), dim3(dg::paged::APPEND_THREADS), 0,
+                    s, 1, p));
+  count_launch();
+  DG_CUDA(cudaGetLastError());
+  return DG_OK;
+}
+
+// Key-range splits of the paged attention: as many as fill the SMs once, each
+// of two tiles at least, none longer than its CTA's page list.  Shape only, so
+// a shape always gives the same bits.
+struct PagedPlan {
+  int n_pairs, tiles_per_split, n_splits;
+};
+
+PagedPlan plan_paged(int B, int Hq, int Hkv, int max_new, long long max_keys) {
+  PagedPlan pl;
+  pl.n_pairs = cdiv(Hq / Hkv * max_new, 2 * dg::paged::BQ);
+  const int tiles = (int)std::max(1ll, (max_keys + dg::paged::BKV - 1) / dg::paged::BKV);
+  const long long units = (long long)B * Hkv * pl.n_pairs;
+  int s = (int)std::max(1ll, kNumSMs / units);
+  s = std::min(s, std::max(1, tiles / 2));
+  pl.tiles_per_split = std::min(cdiv(tiles, s), dg::paged::MAX_TILES);
+  pl.n_splits = cdiv(tiles, pl.tiles_per_split);
+  return pl;
+}
+
+size_t paged_ws_bytes(const PagedPlan& pl, int T, int Hq, int hd) {
+  if (pl.n_splits == 1) return 0;
+  const size_t rows = (size_t)pl.n_splits * T * Hq;
+  return align_up(rows * hd * sizeof(float), 256) + align_up(rows * sizeof(float), 256);
+}
+
+PerDeviceFlag paged_attr_done[2];
+
+template <int HD>
+int launch_paged(const void* k_pages, const void* v_pages, dg::paged::AttnParams p,
+                 const PagedPlan& pl, cudaStream_t s) {
+  using namespace dg::paged;
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)p.bt.n_pages * p.Hkv * p.bt.page;
+  DG_TRY(make_tmap_pages(&tk, k_pages, HD, rows, p.bt.page, true));
+  DG_TRY(make_tmap_pages(&tv, v_pages, HD, rows, p.bt.page, false));
+  if (!paged_attr_done[HD / 128]()) {
+    DG_CUDA(cudaFuncSetAttribute(wide_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Wide<HD>::SMEM_BYTES));
+    paged_attr_done[HD / 128]() = true;
+  }
+  DG_CUDA(launch_ex(wide_kernel<HD>, dim3(p.bt.B * p.Hkv * pl.n_pairs, pl.n_splits),
+                    dim3(WIDE_THREADS), Wide<HD>::SMEM_BYTES, s, 1, tk, tv, p));
+  count_launch();
+  DG_CUDA(cudaGetLastError());
+  if (pl.n_splits > 1) {
+    DG_CUDA(launch_ex(combine_kernel<HD>,
+                      dim3(cdiv(p.bt.max_new * p.Hq, COMBINE_THREADS / 32), p.bt.B),
+                      dim3(COMBINE_THREADS), 0, s, 1, p));
     count_launch();
     DG_CUDA(cudaGetLastError());
   }
@@ -1528,6 +1637,129 @@ int dg_kv_block_commit(const void* const* k_blk, const void* const* v_blk, int l
   count_launch();
   DG_CUDA(cudaGetLastError());
   return DG_OK;
+}
+
+int dg_kv_append_e4m3(const void* k, const void* v, int ldkv, const void* q, int ldq, void* q_out,
+                      int ldqo, int Hq, const float* rope, int rope_len, int rot_dim,
+                      int interleaved, uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exp,
+                      uint8_t* v_exp, int n_pages, int page, const int32_t* page_table,
+                      int max_pages, const int32_t* tok_start, const int32_t* cache_len,
+                      int max_new, int B, int T, int Hkv, int hd, void* stream) {
+  const char* fn = "dg_kv_append_e4m3";
+  if (!k || !v || !k_pages || !v_pages || !k_exp || !v_exp || !page_table || !tok_start ||
+      !cache_len)
+    return fail(DG_ERR_INVALID_ARG, "%s: null pointer", fn);
+  DG_TRY(check_paged(fn, n_pages, page, max_pages, B, T, Hkv, hd, max_new));
+  if ((q != nullptr) != (q_out != nullptr) || (q && Hq < 1))
+    return fail(DG_ERR_INVALID_ARG, "%s: q and q_out go together, with Hq >= 1", fn);
+  if (rot_dim < 0 || rot_dim > hd || rot_dim % 16)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: rot_dim %d is not a multiple of 16 up to %d", fn,
+                rot_dim, hd);
+  if ((rot_dim > 0) != (rope != nullptr) || (rope && rope_len < 1))
+    return fail(DG_ERR_INVALID_ARG, "%s: rot_dim and the angle table go together", fn);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(DG_ERR_INVALID_ARG, "%s: interleaved is 0 or 1", fn);
+  if (q && !rope)
+    return fail(DG_ERR_INVALID_ARG, "%s: q is taken to be rotated, which needs a table", fn);
+  if (ldkv % 8 || ldkv / hd < Hkv || (q && (ldq % 8 || ldqo % 8 || ldq / hd < Hq || ldqo / hd < Hq)))
+    return fail(DG_ERR_ALIGNMENT, "%s: leading dimensions", fn);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(rope) ||
+      !aligned16(k_pages) || !aligned16(v_pages))
+    return fail(DG_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned", fn);
+  if (T == 0 || max_new == 0) return DG_OK;
+  dg::paged::AppendParams p;
+  p.bt = {B, T, std::min(max_new, T), max_pages, page, log2_of(page), n_pages,
+          tok_start, cache_len, page_table};
+  p.Hq = Hq; p.Hkv = Hkv;
+  p.half = rot_dim / 2;
+  p.interleaved = interleaved;
+  p.rope_len = rope_len;
+  p.rope = (const float2*)rope;
+  p.k = (const __nv_bfloat16*)k;
+  p.v = (const __nv_bfloat16*)v;
+  p.q = (const __nv_bfloat16*)q;
+  p.q_out = (__nv_bfloat16*)q_out;
+  p.ldkv = ldkv; p.ldq = ldq; p.ldqo = ldqo;
+  p.k_pages = k_pages; p.v_pages = v_pages; p.k_exp = k_exp; p.v_exp = v_exp;
+  p.slots = (p.bt.max_new + page - 2) / page + 1;
+  p.kv_blocks = cdiv(2 * Hkv, dg::paged::APPEND_THREADS / (2 * page));
+  const long long items =
+      q ? (long long)p.bt.max_new * (hd / 16) * cdiv(Hq, dg::paged::Q_HEADS) : 0;
+  const long long q_blocks = (items + dg::paged::APPEND_THREADS - 1) / dg::paged::APPEND_THREADS;
+  const long long blocks = (long long)B * p.slots * p.kv_blocks + B * q_blocks;
+  if (blocks > 0x7FFFFFFFll || items > 0x7FFFFF00ll)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: too many rows for one launch", fn);
+  p.q_blocks = (int)std::max(1ll, q_blocks);
+  return hd == 128 ? launch_append<128>(p, (int)blocks, (cudaStream_t)stream)
+                   : launch_append<64>(p, (int)blocks, (cudaStream_t)stream);
+}
+
+size_t dg_paged_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int hd, int max_new,
+                                     int max_prefix) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (hd != 64 && hd != 128) ||
+      max_new <= 0 || max_prefix < 0 || (long long)(Hq / Hkv) * std::min(max_new, T) > (1 << 30))
+    return 0;
+  max_new = std::min(max_new, T);
+  return paged_ws_bytes(plan_paged(B, Hq, Hkv, max_new, (long long)max_prefix + max_new), T, Hq,
+                        hd);
+}
+
+int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uint8_t* v_pages,
+                       const uint8_t* k_exp, const uint8_t* v_exp, int n_pages, int page,
+                       const int32_t* page_table, int max_pages, const int32_t* tok_start,
+                       const int32_t* cache_len, int max_new, int max_prefix, void* out, int ldo,
+                       float* lse, int B, int T, int Hq, int Hkv, int hd, float scale,
+                       int mask_mode, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "dg_paged_attn_e4m3";
+  if (!q || !k_pages || !v_pages || !k_exp || !v_exp || !page_table || !tok_start || !cache_len ||
+      !out)
+    return fail(DG_ERR_INVALID_ARG, "%s: null pointer", fn);
+  DG_TRY(check_paged(fn, n_pages, page, max_pages, B, T, Hkv, hd, max_new));
+  if (Hq < 1 || Hq % Hkv || max_prefix < 0 ||
+      (mask_mode != DG_MASK_BIDIR && mask_mode != DG_MASK_CAUSAL))
+    return fail(DG_ERR_INVALID_ARG, "%s: bad sizes or mask", fn);
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(DG_ERR_INVALID_ARG, "%s: the scale must be positive and finite", fn);
+  if (ldq % 8 || ldo % 8 || ldq / hd < Hq || ldo / hd < Hq)
+    return fail(DG_ERR_ALIGNMENT, "%s: leading dimensions", fn);
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages))
+    return fail(DG_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned", fn);
+  max_new = std::min(max_new, T);
+  if ((long long)(Hq / Hkv) * max_new > (1 << 30))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: too many rows per kv head", fn);
+  if (max_new == 0) return DG_OK;
+  // planned from the bounds alone, as the workspace query is
+  const PagedPlan pl = plan_paged(B, Hq, Hkv, max_new, (long long)max_prefix + max_new);
+  if ((long long)B * Hkv * pl.n_pairs > 0x7FFFFFFFll || pl.n_splits > 65535 ||
+      (long long)max_new * Hq > 0x7FFFFF00ll)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: too many rows for one launch", fn);
+  const size_t need = paged_ws_bytes(pl, T, Hq, hd);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(DG_ERR_WORKSPACE_TOO_SMALL, "%s: workspace needs %zu bytes", fn, need);
+  dg::paged::AttnParams p;
+  p.bt = {B, T, max_new, max_pages, page, log2_of(page), n_pages, tok_start, cache_len, page_table};
+  p.Hq = Hq; p.Hkv = Hkv; p.group = Hq / Hkv;
+  p.causal = mask_mode == DG_MASK_CAUSAL ? 1 : 0;
+  p.max_prefix = max_prefix;
+  p.n_pairs = pl.n_pairs;
+  p.tiles_per_split = pl.tiles_per_split;
+  p.n_splits = pl.n_splits;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.q = (const __nv_bfloat16*)q;
+  p.ldq = ldq;
+  p.k_exp = k_exp; p.v_exp = v_exp;
+  p.out = (__nv_bfloat16*)out;
+  p.ldo = ldo;
+  p.lse = lse;
+  p.part_o = nullptr;
+  p.part_lse = nullptr;
+  if (pl.n_splits > 1) {
+    const size_t rows = (size_t)pl.n_splits * T * Hq;
+    p.part_o = (float*)workspace;
+    p.part_lse = (float*)((char*)workspace + align_up(rows * hd * sizeof(float), 256));
+  }
+  return hd == 128 ? launch_paged<128>(k_pages, v_pages, p, pl, (cudaStream_t)stream)
+                   : launch_paged<64>(k_pages, v_pages, p, pl, (cudaStream_t)stream);
 }
 
 size_t dg_prefill_workspace_bytes(const dg_model_cfg* cfg, int B, int P) {

@@ -1,0 +1,694 @@
+// paged_attn.cuh - attention of ragged new rows over a paged e4m3 KV cache.
+//
+// Sequence b's new rows (already appended) attend to its cache_len[b] + n_b
+// cached rows, all of them (canvas) or up to their own position (causal):
+//   s_ij = scale q_i . k_j,   out_i = sum_j softmax_j(s_ij) v_j,
+// with k_j = 2^ek code, v_j = 2^ev code, one exponent per page and kv head.
+// The query rows of a kv head's group are packed token by token (row = token
+// * group + head in group), so a tile holds them whatever the group size.
+//
+// Rounding.  Codes enter the tensor core as they are cached; no key is ever
+// expanded.  A bf16 query row, scaled by a power of two to at most 448, is
+// split into two e4m3 values hi + lo (4 + 4 significant bits: exact for
+// elements down to 2^-10 of the row's largest, below that to 2^-18 of it), and
+// both halves are multiplied by the same key codes with fp32 accumulation.
+// V codes become f16 times a power of two relative to the CTA's largest page
+// scale (exact to 2^-31 of the largest value), and the probabilities f16
+// (2^-11 relative): an 8-bit probability would lose 2^-4.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "attn.cuh"
+#include "dg_common.cuh"
+#include "kvappend.cuh"
+
+namespace dg {
+namespace paged {
+
+constexpr int BQ = 128;
+constexpr int BKV = 128;
+constexpr int MAX_TILES = 128;  // key tiles per CTA: their page ids and scales sit in shared memory
+
+// Order this thread's shared-memory writes before later accesses of the async
+// proxy (the tensor core's operand reads).
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 64-byte-swizzled counterpart of sdesc_sw128 (rows of 64 bytes, 512-byte
+// atoms of 8 rows; 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3)).
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo_bytes,
+                                               uint32_t sbo_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(4) << 61;  // 64-byte swizzle
+  return d;
+}
+
+// Instruction descriptor, kind::f16 with f16 A/B and fp32 D, B MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_bmn(int M, int N) {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Descriptor of a K-major 8-bit tile with rows of HD bytes.
+template <int HD>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr) {
+  if constexpr (HD == 128) return sdesc_sw128(saddr, 16, 1024);
+  return sdesc_sw64(saddr, 16, 512);
+}
+
+// Byte offset of 16-byte chunk c of row r in such a tile.
+template <int HD>
+__device__ __forceinline__ int swz(int r, int c) {
+  if constexpr (HD == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+struct AttnParams {
+  Batch bt;
+  int Hq, Hkv, group, causal;
+  int max_prefix;
+  int n_pairs;           // query-row blocks (of 256 packed rows) per kv head
+  int tiles_per_split;   // key tiles per CTA
+  int n_splits;
+  float scale_log2;      // scale * log2(e)
+  const __nv_bfloat16* q;
+  int ldq;
+  const uint8_t *k_exp, *v_exp;  // [n_pages, Hkv]
+  __nv_bfloat16* out;
+  int ldo;
+  float* lse;       // [T, Hq] or null
+  float* part_o;    // [n_splits, T, Hq, hd] (n_splits > 1)
+  float* part_lse;  // [n_splits, T, Hq]
+};
+
+// Two e4m3 values whose sum is a scaled query element.
+__device__ __forceinline__ void split_q(const float (&x)[8], float f, uint2* hi, uint2* lo) {
+  float h[8], r[8];
+  *hi = pack_e4m3x8(x, f);
+  unpack_e4m3x8(*hi, h);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = fmaf(x[e], f, -h[e]);
+  *lo = pack_e4m3x8(r, 1.f);
+}
+
+// A warp converts rows [r0, r0 + 32) of a tile of packed query rows (first row
+// `first` of `rows` in the kv head's group) to hi / lo tiles, and stores each
+// row's factor scale_log2 * 2^e.  A row that holds an infinity or a NaN gets a
+// NaN factor, so that its scores are NaN; rows past the end are zero.
+template <int HD>
+__device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, int g, int first,
+                                            int rows, uint8_t* hi, uint8_t* lo, float* factor,
+                                            int r0, int n_rows) {
+  constexpr int LANES = HD / 8;        // lanes per row
+  constexpr int PER = 32 / LANES;      // rows per pass
+  constexpr int BATCH = 4;             // passes whose loads are in flight together
+  const int lane = lane_id();
+  const int c8 = lane % LANES;
+  for (int rb = 0; rb < n_rows; rb += PER * BATCH) {
+    uint4 raw[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int r = r0 + rb + u * PER + lane / LANES;
+      const int pr = first + r;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (pr < rows) {
+        const int tok = pr / p.group;
+        raw[u] = *reinterpret_cast<const uint4*>(
+            p.q + static_cast<size_t>(s.t0 + tok) * p.ldq +
+            static_cast<size_t>(g * p.group + pr - tok * p.group) * HD + c8 * 8);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int r = r0 + rb + u * PER + lane / LANES;
+      float x[8];
+      unpack_bf16x8(raw[u], x);
+      float amax = 0.f;
+      bool fine = true;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = fabsf(x[e]);
+        fine = fine && v <= FLT_MAX;
+        amax = fmaxf(amax, v);
+      }
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const uint32_t bad = __ballot_sync(0xffffffffu, !fine);
+      const bool row_fine = ((bad >> (lane & ~(LANES - 1))) & ((1ull << LANES) - 1)) == 0;
+      // 2^e with amax <= 448 2^e; a row of zeros takes e = -100
+      const uint32_t bits = __float_as_uint(amax);
+      const int e = max(static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u), -100);
+      uint2 vh = make_uint2(0u, 0u), vl = make_uint2(0u, 0u);
+      if (row_fine) split_q(x, pow2(-min(e, 126)), &vh, &vl);
+      const int at = swz<HD>(r, c8 >> 1) + (c8 & 1) * 8;
+      *reinterpret_cast<uint2*>(hi + at) = vh;
+      *reinterpret_cast<uint2*>(lo + at) = vl;
+      if (c8 == 0)
+        factor[r] = row_fine ? p.scale_log2 * pow2(min(e, 126)) : __int_as_float(0x7FC00000);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many query rows per kv head: two 128-row query tiles per CTA
+// ---------------------------------------------------------------------------
+// Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer, 2..5 / 6..9 = softmax
+// of tile A / B (one query row per thread), 10..13 = V expansion (codes ->
+// f16 tiles in shared memory, rows past the sequence's end zeroed).
+constexpr int WIDE_THREADS = 448;
+constexpr float P_SHIFT = 7.f;  // probabilities are held as 2^(s - m + 7): at most 2^15 in f16
+constexpr int V_SHIFT = 7;      // V codes as code 2^(ev - emax + 7): at most 57344 in f16
+
+template <int HD>
+struct Wide {
+  static constexpr int T_BYTES = BKV * HD;       // K or V codes of a tile; also a hi or lo tile of Q
+  static constexpr int V16_BYTES = BKV * HD * 2;
+  static constexpr int KST = 3, VST = 2, HST = 2;  // stages of K codes, V codes, V f16
+  static constexpr int RING = KST * T_BYTES + VST * T_BYTES + HST * V16_BYTES;
+  static constexpr int MAX_PAGES = MAX_TILES * (BKV / 16);
+  static constexpr int SMEM_BYTES = 1024 + 4 * T_BYTES + RING + MAX_PAGES * 9 + 2 * BQ * 4 + 512;
+  static constexpr uint32_t IDESC_S = idesc_e4m3_f32(BQ, BKV);
+  static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(BQ, HD);
+  static_assert(RING >= 2 * BQ * HD * 4, "O staging does not fit the rings");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+template <int HD>
+__global__ void __launch_bounds__(WIDE_THREADS, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ AttnParams p) {
+  using CF = Wide<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;                              // [2 tiles][hi, lo]
+  uint8_t* sV16 = sQ + 4 * CF::T_BYTES;            // HST tiles [halves][128][128 B]
+  uint8_t* sK = sV16 + CF::HST * CF::V16_BYTES;    // KST tiles, swizzled
+  uint8_t* sV8 = sK + CF::KST * CF::T_BYTES;       // VST tiles, plain rows
+  float* sQf = reinterpret_cast<float*>(sV8 + CF::VST * CF::T_BYTES);  // [256] row factors
+  float* sKf = sQf + 2 * BQ;                                           // [MAX_PAGES] 2^ek
+  int* sPage = reinterpret_cast<int*>(sKf + CF::MAX_PAGES);            // [MAX_PAGES]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sPage + CF::MAX_PAGES);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = q_full + 1;              // [KST]
+  uint64_t* k_empty = k_full + CF::KST;       // [KST]
+  uint64_t* v8_full = k_empty + CF::KST;      // [VST]
+  uint64_t* v8_empty = v8_full + CF::VST;     // [VST]
+  uint64_t* v16_full = v8_empty + CF::VST;    // [HST]
+  uint64_t* v16_empty = v16_full + CF::HST;   // [HST]
+  uint64_t* s_full = v16_empty + CF::HST;     // [2] per query tile
+  uint64_t* p_full = s_full + 2;              // [2]
+  uint64_t* o_final = p_full + 2;
+  uint64_t* drain = o_final + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* s_emax = reinterpret_cast<int*>(tmem_holder + 2);
+  uint8_t* sVe = reinterpret_cast<uint8_t*>(tmem_holder + 4);  // [MAX_PAGES] biased ev
+
+  const int warp = warp_id();
+  const int lane = lane_id();
+  griddep_launch();
+  griddep_wait();
+  const Batch& bt = p.bt;
+  const int pi = static_cast<int>(blockIdx.x) % p.n_pairs;
+  const int gb = static_cast<int>(blockIdx.x) / p.n_pairs;
+  const int g = gb % p.Hkv;
+  const int b = gb / p.Hkv;
+  const int split = blockIdx.y;
+  const Seq s = load_seq(bt, b, p.max_prefix, 0x511,
+                         threadIdx.x == 0 && split == 0 && pi == 0 && g == 0);
+  const int rows = s.n * p.group;
+  const int first = pi * 2 * BQ;
+  if (first >= rows) return;
+  const bool vB = first + BQ < rows;
+  const int total = s.c0 + s.n;
+  const int last_tok = (min(rows, first + 2 * BQ) - 1) / p.group;
+  const int visible = p.causal ? s.c0 + last_tok + 1 : total;  // keys that this CTA's rows see
+  const int tiles = (visible + BKV - 1) / BKV;
+  const int t_beg = split * p.tiles_per_split;
+  const int n = min(tiles, t_beg + p.tiles_per_split) - t_beg;
+  if (n <= 0) return;
+  const int log_ppt = 7 - bt.log_page;  // log2(pages per tile)
+  const int page_beg = t_beg << log_ppt;
+  const int n_pages = ((min(visible, (t_beg + n) * BKV) + bt.page - 1) >> bt.log_page) - page_beg;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, vB ? 8 : 4);
+    for (int i = 0; i < CF::KST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < CF::VST; ++i) {
+      mbar_init(&v8_full[i], 1);
+      mbar_init(&v8_empty[i], 4);
+    }
+    for (int i = 0; i < CF::HST; ++i) {
+      mbar_init(&v16_full[i], 4);
+      mbar_init(&v16_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], BQ);
+    }
+    mbar_init(o_final, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *s_emax = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  // page ids and scales of the whole key range
+  int emax = 0;
+  for (int i = threadIdx.x; i < (n << log_ppt); i += WIDE_THREADS) {
+    int pg = -1;
+    float kf = 1.f;
+    int ve = 0;
+    if (i < n_pages) {
+      pg = bt.page_table[static_cast<size_t>(b) * bt.max_pages + page_beg + i];
+      if (pg < 0 || pg >= bt.n_pages) {
+        raise_error(ERR_CHECK | 0x512, static_cast<uint32_t>(b));
+        pg = -1;
+      } else {
+        const size_t at = static_cast<size_t>(pg) * p.Hkv + g;
+        kf = __uint_as_float(static_cast<uint32_t>(p.k_exp[at]) << 23);
+        ve = p.v_exp[at];
+      }
+    }
+    sPage[i] = pg;
+    sKf[i] = kf;
+    sVe[i] = static_cast<uint8_t>(ve);
+    emax = max(emax, ve);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  emax = __reduce_max_sync(0xffffffffu, emax);
+  if (lane == 0 && emax > 0) atomicMax(s_emax, emax);
+  __syncthreads();
+  emax = *s_emax;
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    // Lane l loads page l of the tile.  A page outside the table's range was
+    // reported above; it is read as zeros (a box past the tensor's end).
+    const int ppt = 1 << log_ppt;
+    const int page_bytes = bt.page * HD;
+    int issued = 0;
+    for (int j = 0; j < n; ++j) {
+      const int ks = j % CF::KST, vs = j % CF::VST;
+      bool ok = j < CF::KST || mbar_wait(&k_empty[ks], ((j / CF::KST) - 1) & 1, abort_flag, 0x521);
+      ok = ok && (j < CF::VST ||
+                  mbar_wait(&v8_empty[vs], ((j / CF::VST) - 1) & 1, abort_flag, 0x522));
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int pages = min(ppt, n_pages - (j << log_ppt));
+      if (lane == 0) {
+        mbar_expect_tx(&k_full[ks], pages * page_bytes);
+        mbar_expect_tx(&v8_full[vs], pages * page_bytes);
+      }
+      __syncwarp();
+      if (lane < pages) {
+        const int pg = sPage[(j << log_ppt) + lane];
+        const int y = pg < 0 ? bt.n_pages * p.Hkv * bt.page : (pg * p.Hkv + g) * bt.page;
+        tma_load_2d(sK + ks * CF::T_BYTES + lane * page_bytes, &tm_k, &k_full[ks], 0, y);
+        tma_load_2d(sV8 + vs * CF::T_BYTES + lane * page_bytes, &tm_v, &v8_full[vs], 0, y);
+      }
+      issued = j + 1;
+    }
+    if (*abort_flag && lane == 0) {
+      for (int j = max(0, issued - CF::KST); j < issued; ++j)
+        mbar_wait(&k_full[j % CF::KST], (j / CF::KST) & 1, nullptr, 0x523);
+      for (int j = max(0, issued - CF::VST); j < issued; ++j)
+        mbar_wait(&v8_full[j % CF::VST], (j / CF::VST) & 1, nullptr, 0x524);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = mbar_wait(q_full, 0, abort_flag, 0x531);
+      const uint32_t q_base = smem_u32(sQ);
+      auto issue_s = [&](int X, int j) {  // S_X = (hi + lo) K^T
+        const uint32_t k_base = smem_u32(sK + (j % CF::KST) * CF::T_BYTES);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < HD / 32; ++kk)
+            umma_ss_f8(tmem + X * 128,
+                       sdesc_rows<HD>(q_base + (2 * X + part) * CF::T_BYTES + kk * 32),
+                       sdesc_rows<HD>(k_base + kk * 32), CF::IDESC_S, (part | kk) ? 1u : 0u);
+        umma_commit(&s_full[X]);
+      };
+      auto issue_pv = [&](int X, int j) -> bool {
+        if (!mbar_wait(&p_full[X], j & 1, abort_flag, 0x533)) return false;
+        tc_fence_after();
+        const uint32_t v_base = smem_u32(sV16 + (j % CF::HST) * CF::V16_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < BKV / 16; ++kk)
+          umma_ts(tmem + 256 + X * 128, tmem + X * 128 + kk * 8,
+                  sdesc_sw128(v_base + kk * 16 * 128, BKV * 128, 1024), CF::IDESC_PV,
+                  (j | kk) ? 1u : 0u);
+        return true;
+      };
+      if (ok) ok = mbar_wait(&k_full[0], 0, abort_flag, 0x532);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        if (vB) issue_s(1, 0);
+        umma_commit(&k_empty[0]);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        ok = mbar_wait(&v16_full[j % CF::HST], (j / CF::HST) & 1, abort_flag, 0x534);
+        if (ok) ok = issue_pv(0, j);
+        const bool more = j + 1 < n;
+        const int ks = (j + 1) % CF::KST;
+        if (ok && more) {
+          ok = mbar_wait(&k_full[ks], ((j + 1) / CF::KST) & 1, abort_flag, 0x532);
+          if (ok) {
+            tc_fence_after();
+            issue_s(0, j + 1);
+          }
+        }
+        if (ok && vB) ok = issue_pv(1, j);
+        if (ok) umma_commit(&v16_empty[j % CF::HST]);
+        if (ok && more) {
+          if (vB) issue_s(1, j + 1);
+          umma_commit(&k_empty[ks]);
+        }
+      }
+      if (ok) umma_commit(o_final);
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, 0x535);
+    }
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ V expansion
+    const int tid = static_cast<int>(threadIdx.x) - 320;
+    constexpr int CPR = HD / 16;            // 16-code chunks per row
+    constexpr int RSTEP = 128 / CPR;        // rows per pass
+    constexpr int PASSES = BKV / RSTEP;
+    const int c = tid % CPR;
+    const int r0 = tid / CPR;
+    // 16 codes -> two 16-byte chunks 2 (c % 4), + 1 of half c / 4, swizzled;
+    // the halves write their chunks in opposite order (no bank conflicts)
+    const int half_off = (c >> 2) * (BKV * 128);
+    const int odd = (c >> 2) & 1;
+    const int ch0 = (2 * (c & 3)) | odd;
+    for (int j = 0; j < n; ++j) {
+      const int vs = j % CF::VST, hs = j % CF::HST;
+      bool ok = mbar_wait(&v8_full[vs], (j / CF::VST) & 1, abort_flag, 0x541);
+      ok = ok && (j < CF::HST ||
+                  mbar_wait(&v16_empty[hs], ((j / CF::HST) - 1) & 1, abort_flag, 0x542));
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* src = sV8 + vs * CF::T_BYTES;
+      uint8_t* dst = sV16 + hs * CF::V16_BYTES + half_off;
+      const int live = visible - (t_beg + j) * BKV;  // rows of this tile that were loaded
+#pragma unroll
+      for (int u = 0; u < PASSES; ++u) {
+        const int r = r0 + u * RSTEP;
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+        if (r < live) {
+          const int k = static_cast<int>(sVe[(j << log_ppt) + (r >> bt.log_page)]) - emax + V_SHIFT;
+          const uint32_t fb = k >= -14 ? static_cast<uint32_t>(k + 15) << 10
+                                       : (k >= -24 ? 1u << (k + 24) : 0u);
+          const __half2 f = __half2(__ushort_as_half(static_cast<unsigned short>(fb)),
+                                    __ushort_as_half(static_cast<unsigned short>(fb)));
+          const uint4 raw = *reinterpret_cast<const uint4*>(src + r * HD + c * 16);
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu),
+                __NV_E4M3));
+            const __half2 m = __hmul2(h, f);
+            o[e] = *reinterpret_cast<const uint32_t*>(&m);
+          }
+          lo = make_uint4(o[0], o[1], o[2], o[3]);
+          hi = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        uint8_t* row = dst + r * 128;
+        *reinterpret_cast<uint4*>(row + ((ch0 ^ (r & 7)) << 4)) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(row + (((ch0 ^ 1) ^ (r & 7)) << 4)) = odd ? lo : hi;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&v16_full[hs]);
+        mbar_arrive(&v8_empty[vs]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax (tile X)
+    const int X = (warp - 2) >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int qrow = first + X * BQ + r;  // packed row
+    const bool mine = X == 0 || vB;
+    if (mine) {
+      load_q_rows<HD>(p, s, g, first + X * BQ, rows, sQ + 2 * X * CF::T_BYTES,
+                      sQ + (2 * X + 1) * CF::T_BYTES, sQf + X * BQ, quarter * 32, 32);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + X * 128 + lane_off;
+    const uint32_t tO = tmem + 256 + X * 128 + lane_off;
+    float m = -INFINITY;  // running max in log2 units
+    float l = 0.f;
+    bool ok = mine;
+    const float sc = mine ? sQf[X * BQ + r] : 0.f;
+    // keys [0, sees) are visible to this row
+    const int sees = p.causal ? min(total, s.c0 + qrow / p.group + 1) : total;
+    for (int j = 0; j < n && ok; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[X], j & 1, abort_flag, 0x551))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int lim = sees - (t_beg + j) * BKV - 1;  // columns [0, lim] are visible
+      const bool masked = __any_sync(0xffffffffu, lim < BKV - 1);
+      float scg[8];  // row factor times the page scale, per 16 columns
+#pragma unroll
+      for (int q = 0; q < 8; ++q) scg[q] = sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)];
+      float tmax = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t sa[32];
+        tmem_ld32(tS + h * 32, sa);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h * 32 + c > lim) sa[c] = __float_as_uint(-INFINITY);
+        }
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          m0 = fmaxf(m0, __uint_as_float(sa[c]));
+          m1 = fmaxf(m1, __uint_as_float(sa[16 + c]));
+        }
+        tmax = fmaxf(tmax, fmaxf(m0 * scg[2 * h], m1 * scg[2 * h + 1]));
+      }
+      // Raise the running max only when it grows by more than 2^8 (1/l keeps
+      // this exact).  PV_X(j-1) is complete because S_X(j) is.
+      const bool want = tmax > m + attn::kRescaleThreshold || m == -INFINITY;
+      if (__any_sync(0xffffffffu, want)) {
+        const float m_new = fmaxf(tmax, m);
+        if (j > 0) {
+          const float f = (m == -INFINITY) ? 0.f : attn::fast_exp2(m - m_new);
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tO + c * 32, o);
+          }
+          l *= f;
+        }
+        m = m_new;
+      }
+      const float neg_m = (m == -INFINITY) ? 0.f : P_SHIFT - m;
+      float rs0 = 0.f, rs1 = 0.f, rs2 = 0.f, rs3 = 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t sa[32];
+        tmem_ld32(tS + h * 32, sa);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h * 32 + c > lim) sa[c] = __float_as_uint(-INFINITY);
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          const float f = scg[2 * h + (c >> 3)];
+          const float p0 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c]), f, neg_m));
+          const float p1 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c + 1]), f, neg_m));
+          const float p2 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c + 2]), f, neg_m));
+          const float p3 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c + 3]), f, neg_m));
+          rs0 += p0;
+          rs1 += p1;
+          rs2 += p2;
+          rs3 += p3;
+          const __half2 a = __floats2half2_rn(p0, p1), d = __floats2half2_rn(p2, p3);
+          pk[c] = *reinterpret_cast<const uint32_t*>(&a);
+          pk[c + 1] = *reinterpret_cast<const uint32_t*>(&d);
+        }
+        // P overwrites S: 32 scores become 16 columns, always behind the reads
+        tmem_st16(tS + h * 16, pk);
+      }
+      l += (rs0 + rs1) + (rs2 + rs3);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[X]);
+    }
+    const bool fin = __all_sync(0xffffffffu, ok && mbar_wait(o_final, 0, abort_flag, 0x553));
+    // Stage O_X in the idle rings (rows XOR-swizzled by 16-byte chunk), then
+    // write whole rows: coalesced stores, fp32 partials or bf16 results.
+    float* stage = reinterpret_cast<float*>(sV16) + X * (BQ * HD);
+    const int tok_r = qrow / p.group;
+    const int h_r = g * p.group + qrow - tok_r * p.group;
+    // probabilities carry 2^P_SHIFT in O and in l alike; V carries 2^(V_SHIFT - emax)
+    const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(emax - 127 - V_SHIFT)) / l;
+    const float lse_nat =
+        l == 0.f ? -INFINITY : (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
+    if (fin) {
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const int chunk = (c * 8 + v) ^ (r & 7);
+          reinterpret_cast<float4*>(stage + r * HD)[chunk] =
+              make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                          __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+        }
+      }
+      if (qrow < rows) {
+        const size_t at = static_cast<size_t>(s.t0 + tok_r) * p.Hq + h_r;
+        if (p.n_splits == 1) {
+          if (p.lse) p.lse[at] = lse_nat;
+        } else {
+          p.part_lse[static_cast<size_t>(split) * bt.T * p.Hq + at] = lse_nat;
+        }
+      }
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + X), "r"(BQ) : "memory");
+    if (fin) {
+      constexpr int CPR = HD / 4;
+      constexpr int RPW = 32 / CPR == 0 ? 1 : 32 / CPR;  // rows per warp and pass
+      const int cc = lane % CPR;
+      for (int rr = quarter * RPW + lane / CPR; rr < BQ; rr += 4 * RPW) {
+        const int pr = first + X * BQ + rr;
+        if (pr >= rows) break;
+        const int tok = pr / p.group;
+        const int h = g * p.group + pr - tok * p.group;
+        const float4 v = reinterpret_cast<const float4*>(stage + rr * HD)[cc ^ (rr & 7)];
+        if (p.n_splits == 1) {
+          *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(s.t0 + tok) * p.ldo +
+                                    static_cast<size_t>(h) * HD + cc * 4) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        } else {
+          const size_t row = (static_cast<size_t>(split) * bt.T + s.t0 + tok) * p.Hq + h;
+          reinterpret_cast<float4*>(p.part_o + row * HD)[cc] = v;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the key-range splits: out = sum_s w_s O_s / sum_s w_s with
+// w_s = 2^(lse_s - max).  A warp per (token, head); only the splits that the
+// row's visible keys reach were written, and only those are read, in order.
+// ---------------------------------------------------------------------------
+constexpr int COMBINE_THREADS = 256;
+constexpr int COMBINE_BATCH = 8;
+
+template <int HD>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnParams p) {
+  constexpr int PER = HD / 32;
+  griddep_launch();
+  griddep_wait();
+  const int b = blockIdx.y;
+  const int lane = lane_id();
+  const int item = static_cast<int>(blockIdx.x) * (COMBINE_THREADS / 32) + warp_id();
+  const Seq s = load_seq(p.bt, b, p.max_prefix, 0x511, false);
+  const int tok = item / p.Hq;
+  if (tok >= s.n) return;
+  const int h = item - tok * p.Hq;
+  const int sees = p.causal ? s.c0 + tok + 1 : s.c0 + s.n;
+  const int S = (((sees + BKV - 1) / BKV) + p.tiles_per_split - 1) / p.tiles_per_split;
+  const size_t row = static_cast<size_t>(s.t0 + tok) * p.Hq + h;
+  const size_t stride = static_cast<size_t>(p.bt.T) * p.Hq;
+  float mx = -INFINITY, wsum = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < S; s0 += COMBINE_BATCH) {
+    float ls[COMBINE_BATCH], v[COMBINE_BATCH][PER];
+#pragma unroll
+    for (int k = 0; k < COMBINE_BATCH; ++k) {
+      const int sp = s0 + k;
+      ls[k] = sp < S ? p.part_lse[sp * stride + row] : -INFINITY;
+      const float* src = p.part_o + (sp * stride + row) * HD + lane * PER;
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) {
+        const float2 f = sp < S ? *reinterpret_cast<const float2*>(src + e) : make_float2(0.f, 0.f);
+        v[k][e] = f.x;
+        v[k][e + 1] = f.y;
+      }
+    }
+    float top = mx;
+#pragma unroll
+    for (int k = 0; k < COMBINE_BATCH; ++k) top = fmaxf(top, ls[k]);
+    if (top > mx) {
+      const float f = mx == -INFINITY ? 0.f : expf(mx - top);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] *= f;
+      wsum *= f;
+      mx = top;
+    }
+#pragma unroll
+    for (int k = 0; k < COMBINE_BATCH; ++k) {
+      if (ls[k] == -INFINITY) continue;  // no visible key in the split
+      const float w = expf(ls[k] - mx);
+      wsum += w;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+    }
+  }
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+  __nv_bfloat16* out = p.out + static_cast<size_t>(s.t0 + tok) * p.ldo +
+                       static_cast<size_t>(h) * HD + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2)
+    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = wsum == 0.f ? -INFINITY : mx + logf(wsum);
+}
+
+}  // namespace paged
+}  // namespace dg

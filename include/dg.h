@@ -281,6 +281,94 @@ int dg_canvas_attn_e4m3(const uint8_t* q, int ldq, const float* q_scale, const u
                         int mask_mode, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Paged e4m3 KV cache.  The cache that dg_kv_append_e4m3 writes and
+ * dg_paged_attn_e4m3 reads holds half the bytes of a bf16 cache, in pages that
+ * a caller's allocator hands out, for sequences of unequal length:
+ *   k_pages, v_pages  e4m3 codes [n_pages, Hkv, page, hd], page in {16, 32, 64, 128}
+ *   k_exp, v_exp      uint8 [n_pages, Hkv]: a page's rows of one kv head share
+ *                     the scale 2^(exp - 127); value = code * scale
+ *   page_table        int32 [B, max_pages]: position p of sequence b lies in row
+ *                     p % page of page page_table[b, p / page]
+ * New rows are packed: sequence b's are the token rows tok_start[b] ..
+ * tok_start[b + 1] - 1 of the [T, ...] tensors (int32 [B + 1], not decreasing,
+ * tok_start[B] <= T; token rows outside are neither read nor written), and
+ * they take the positions cache_len[b], cache_len[b] + 1, ... (int32 [B], the
+ * rows cached before them).  A sequence may have no new rows.  max_new is a
+ * host bound on every sequence's new rows, used to plan the launch.
+ * The arrays tok_start, cache_len and page_table are read on the device; a
+ * sequence that does not fit max_new, T or its max_pages pages, or a page id
+ * outside [0, n_pages) that is needed, is reported by
+ * dg_check_device_errors() as DG_ERR_DEVICE_CHECK; the sequence's rows are
+ * then left out (a page that does not exist is not written, and read as
+ * zeros), and no memory outside the given buffers is touched.  page_table entries past a sequence's last row are not read.
+ * A step of a denoising loop appends its canvas at cache_len, attends with
+ * DG_MASK_BIDIR and leaves cache_len as it is, so that the next step writes
+ * the same positions again; a decoding step appends one row, attends with
+ * DG_MASK_CAUSAL and raises cache_len.  Both calls may be captured into a graph.
+ *
+ * dg_kv_append_e4m3 - rotate new keys (and queries) by their positions and
+ * store the new keys and values.
+ *   k, v   bf16 [T, ldkv], kv head g at columns g*hd
+ *   q      bf16 [T, ldq] or NULL, query head h at columns h*hd; q_out bf16
+ *          [T, ldqo] gets the rotated queries (q_out may be q)
+ *   rope   fp32 [rope_len, rot_dim / 2, 2]: cos and sin of the angle of
+ *          (position, pair); NULL with rot_dim 0 for no rotation (q then NULL).
+ *          The first rot_dim (a multiple of 16) elements of a head rotate in
+ *          the pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1:
+ *          (x, y) -> (x cos - y sin, y cos + x sin), in fp32 with every product
+ *          and sum rounded.  A sequence whose positions reach rope_len is
+ *          reported as above.
+ * Scale of a page and kv head: 2^e with e the smallest integer for which the
+ * page's new rows satisfy max |x| <= 448 2^e (infinities and NaN left out),
+ * within [-40, 100]; where rows of earlier appends stay in the page (positions
+ * below cache_len), e is at least their old scale's, and their codes are
+ * rounded again (nearest, ties to even) if it grew.  Codes: x / 2^e, nearest e4m3
+ * value, ties to even, saturating at 448; NaN stays NaN.  Rows of a page
+ * behind the last new one are left as they are.
+ * A page that is written must belong to one sequence (pages that are full and
+ * only read may be shared); page ids that appear twice among the written ones
+ * leave that page's contents undefined.  Needs no workspace.
+ */
+int dg_kv_append_e4m3(const void* k, const void* v, int ldkv, const void* q, int ldq, void* q_out,
+                      int ldqo, int Hq, const float* rope, int rope_len, int rot_dim,
+                      int interleaved, uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exp,
+                      uint8_t* v_exp, int n_pages, int page, const int32_t* page_table,
+                      int max_pages, const int32_t* tok_start, const int32_t* cache_len,
+                      int max_new, int B, int T, int Hkv, int hd, void* stream);
+
+/*
+ * dg_paged_attn_e4m3 - attention of the new rows (whose keys and values were
+ * appended before) over everything cached of their sequence:
+ *   out[t,h,:] = softmax_j(q[t,h,:] . key_j * scale) value_j, over positions
+ *   j < cache_len[b] + n_b (DG_MASK_BIDIR) or j <= the row's own position
+ *   (DG_MASK_CAUSAL), kv head h / (Hq/Hkv).
+ *   q    bf16 [T, ldq], head h at columns h*hd (rotated already, if at all)
+ *   out  bf16 [T, ldo];  lse fp32 [T, Hq] natural-log sum of exp of the scaled
+ *        scores, or NULL
+ *   max_prefix: host bound on every cache_len[b] (with max_new it sets the
+ *   split over keys; a larger length is reported like the errors above)
+ * Queries enter the product at bf16 precision (a row's elements below 2^-10 of
+ * its largest to 2^-18 of that), key and value codes as they are cached,
+ * probabilities rounded to f16 or finer; sums and softmax statistics are fp32.
+ * Values more than 2^31 below the largest page scale among a sequence's pages
+ * may be lost.  Exponents must lie in [1, 254].  Positions from
+ * cache_len[b] + n_b on may hold any codes, NaN among them.  A NaN or an
+ * infinity in a query row makes that row NaN; a NaN code at a cached position
+ * makes NaN of the rows that see it, and may of earlier rows of its sequence.
+ * Requires Hq % Hkv == 0, ldq and ldo multiples of 8, scale > 0.
+ * Workspace: dg_paged_attn_workspace_bytes(); calls that may run at the same
+ * time (other streams, other captured graphs) need workspaces of their own.
+ */
+int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uint8_t* v_pages,
+                       const uint8_t* k_exp, const uint8_t* v_exp, int n_pages, int page,
+                       const int32_t* page_table, int max_pages, const int32_t* tok_start,
+                       const int32_t* cache_len, int max_new, int max_prefix, void* out, int ldo,
+                       float* lse, int B, int T, int Hq, int Hkv, int hd, float scale,
+                       int mask_mode, void* workspace, size_t workspace_bytes, void* stream);
+size_t dg_paged_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int hd, int max_new,
+                                     int max_prefix);
+
+/*
  * dg_unembed - vocabulary logits of the normalised final hidden states (the
  * "diffusion head" of aiexpert.news architecture paragraph; untied).
  *   logits[m, v] = sum_k h[m, k] w_u[v, k]

@@ -16,6 +16,7 @@ Modules:
   loop     the block-autoregressive loop composed from the two.
   fp8      e4m3 encoding from the format's definition, per-row / per-tensor
            scaling, and the FP8 unembedding's logits.
+  paged    a paged e4m3 KV cache: append with position rotation, attention.
 
 Parity status: every function is pinned by a test under tests/ against the
 pages' fixed settings, closed forms, library routines or invariants, except
