@@ -691,17 +691,34 @@ int launch_append(const dg::paged::AppendParams& p, int blocks, cudaStream_t s) 
   return DG_OK;
 }
 
-// Key-range splits of the paged attention: as many as fill the SMs once, each
-// of two tiles at least, none longer than its CTA's page list.  Shape only, so
-// a shape always gives the same bits.
+// Execution plan of the paged attention, from the shape's bounds alone (so a
+// shape always gives the same bits).  Up to 32 packed rows per kv head run with
+// keys along the tensor core's M (narrow_kernel, `rows` = 16 or 32), more with
+// 256-row query blocks (wide_kernel, rows = 0).  The key range is split so that
+// the SMs are filled once (wide; splits of two tiles at least), or a few times
+// over (narrow, two CTAs per SM: unequal lengths then even out).
 struct PagedPlan {
-  int n_pairs, tiles_per_split, n_splits;
+  int rows, n_pairs, tiles_per_split, n_splits;
 };
 
 PagedPlan plan_paged(int B, int Hq, int Hkv, int max_new, long long max_keys) {
   PagedPlan pl;
-  pl.n_pairs = cdiv(Hq / Hkv * max_new, 2 * dg::paged::BQ);
+  const int rows = Hq / Hkv * max_new;
   const int tiles = (int)std::max(1ll, (max_keys + dg::paged::BKV - 1) / dg::paged::BKV);
+  if (rows <= 32) {
+    pl.rows = rows <= 16 ? 16 : 32;
+    pl.n_pairs = 1;
+    const long long units = (long long)B * Hkv;
+    static const int slots = getenv("DG_NSLOTS") ? atoi(getenv("DG_NSLOTS")) : 2 * kNumSMs;
+    static const int most = getenv("DG_NMOST") ? atoi(getenv("DG_NMOST")) : 16;
+    const long long even = (units * tiles + slots - 1) / slots;
+    const int per = (int)std::min<long long>(std::max(1ll, even), most);
+    pl.tiles_per_split = cdiv(tiles, cdiv(tiles, per));
+    pl.n_splits = cdiv(tiles, pl.tiles_per_split);
+    return pl;
+  }
+  pl.rows = 0;
+  pl.n_pairs = cdiv(rows, 2 * dg::paged::BQ);
   const long long units = (long long)B * Hkv * pl.n_pairs;
   int s = (int)std::max(1ll, kNumSMs / units);
   s = std::min(s, std::max(1, tiles / 2));
@@ -716,7 +733,7 @@ size_t paged_ws_bytes(const PagedPlan& pl, int T, int Hq, int hd) {
   return align_up(rows * hd * sizeof(float), 256) + align_up(rows * sizeof(float), 256);
 }
 
-PerDeviceFlag paged_attr_done[2];
+PerDeviceFlag paged_attr_done[2][3];
 
 template <int HD>
 int launch_paged(const void* k_pages, const void* v_pages, dg::paged::AttnParams p,
@@ -725,14 +742,26 @@ int launch_paged(const void* k_pages, const void* v_pages, dg::paged::AttnParams
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)p.bt.n_pages * p.Hkv * p.bt.page;
   DG_TRY(make_tmap_pages(&tk, k_pages, HD, rows, p.bt.page, true));
-  DG_TRY(make_tmap_pages(&tv, v_pages, HD, rows, p.bt.page, false));
-  if (!paged_attr_done[HD / 128]()) {
-    DG_CUDA(cudaFuncSetAttribute(wide_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Wide<HD>::SMEM_BYTES));
-    paged_attr_done[HD / 128]() = true;
+  // the expanding kernel reads V rows plainly, the other as an operand tile
+  DG_TRY(make_tmap_pages(&tv, v_pages, HD, rows, p.bt.page, pl.rows != 0));
+  decltype(&wide_kernel<HD>) kernel = wide_kernel<HD>;
+  int threads = WIDE_THREADS, smem = Wide<HD>::SMEM_BYTES;
+  if (pl.rows == 16) {
+    kernel = narrow_kernel<HD, 16>;
+    threads = NARROW_THREADS;
+    smem = Narrow<HD, 16>::SMEM_BYTES;
+  } else if (pl.rows == 32) {
+    kernel = narrow_kernel<HD, 32>;
+    threads = NARROW_THREADS;
+    smem = Narrow<HD, 32>::SMEM_BYTES;
   }
-  DG_CUDA(launch_ex(wide_kernel<HD>, dim3(p.bt.B * p.Hkv * pl.n_pairs, pl.n_splits),
-                    dim3(WIDE_THREADS), Wide<HD>::SMEM_BYTES, s, 1, tk, tv, p));
+  bool& attr_set = paged_attr_done[HD / 128][pl.rows / 16]();
+  if (!attr_set) {
+    DG_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    attr_set = true;
+  }
+  DG_CUDA(launch_ex(kernel, dim3(p.bt.B * p.Hkv * pl.n_pairs, pl.n_splits), dim3(threads), smem, s,
+                    1, tk, tv, p));
   count_launch();
   DG_CUDA(cudaGetLastError());
   if (pl.n_splits > 1) {

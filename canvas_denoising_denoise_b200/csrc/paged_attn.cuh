@@ -98,7 +98,7 @@ __device__ __forceinline__ void split_q(const float (&x)[8], float f, uint2* hi,
   *lo = pack_e4m3x8(r, 1.f);
 }
 
-// A warp converts rows [r0, r0 + 32) of a tile of packed query rows (first row
+// A warp converts rows [r0, r0 + n_rows) of a tile of packed query rows (first row
 // `first` of `rows` in the kv head's group) to hi / lo tiles, and stores each
 // row's factor scale_log2 * 2^e.  A row that holds an infinity or a NaN gets a
 // NaN factor, so that its scores are NaN; rows past the end are zero.
@@ -118,7 +118,7 @@ __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, i
       const int r = r0 + rb + u * PER + lane / LANES;
       const int pr = first + r;
       raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (pr < rows) {
+      if (pr < rows && r < r0 + n_rows) {
         const int tok = pr / p.group;
         raw[u] = *reinterpret_cast<const uint4*>(
             p.q + static_cast<size_t>(s.t0 + tok) * p.ldq +
@@ -148,6 +148,7 @@ __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, i
       const int e = max(static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u), -100);
       uint2 vh = make_uint2(0u, 0u), vl = make_uint2(0u, 0u);
       if (row_fine) split_q(x, pow2(-min(e, 126)), &vh, &vl);
+      if (r >= r0 + n_rows) continue;
       const int at = swz<HD>(r, c8 >> 1) + (c8 & 1) * 8;
       *reinterpret_cast<uint2*>(hi + at) = vh;
       *reinterpret_cast<uint2*>(lo + at) = vl;
@@ -215,7 +216,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
   const int warp = warp_id();
   const int lane = lane_id();
-  griddep_launch();
   griddep_wait();
   const Batch& bt = p.bt;
   const int pi = static_cast<int>(blockIdx.x) % p.n_pairs;
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch();  // only now: a successor's CTA must not take the TMEM before this one
   emax = __reduce_max_sync(0xffffffffu, emax);
   if (lane == 0 && emax > 0) atomicMax(s_emax, emax);
   __syncthreads();
@@ -618,6 +619,470 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few query rows per kv head (decoding): keys along the tensor core's M
+// ---------------------------------------------------------------------------
+// With R = group * n_b <= 32 rows a 128-row query tile would be mostly padding,
+// and one softmax thread would walk all 128 keys of a tile alone.  So the
+// products are transposed: per tile of 128 keys
+//     S^T [keys x 2 NR]  = K [hi | lo]^T      A = K tile, B = query halves
+//     O^T [hd x 4 NR]   += V^T [p0 p1 p2 0]   A = V tile (M-major), B = P
+// NR (16 or 32) holds the rows.  A thread owns one key: its page's scales are
+// per-thread constants and its NR probabilities are 3 x NR bytes, one 16-byte
+// store per 16.  A probability p (times the page's V scale) enters as three
+// e4m3 terms p0 + p1/16 + p2/256, each the rounding of what the terms before
+// left: 11 bits of it, down to 2^-22 of the largest.  Both products read the
+// codes as TMA delivered them: the kernel streams the cache and does nothing
+// else to it, and is bound by HBM once there are enough keys.
+//
+// The running maximum m is common to all keys of the CTA and only raised when
+// a score would pass 2^8.5 (p carries 2^4): the test costs one barrier with an
+// OR a tile, the raise itself (shuffles, rescaling O) is rare.
+//
+// Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer, 2..5 = softmax (thread
+// = key; at the end thread = element of the head).
+constexpr int NARROW_THREADS = 192;
+constexpr float N_SHIFT = 4.f;
+constexpr float N_LIMIT = 8.5f;  // 2^8.5 = 362 <= 448
+
+template <int HD, int NR>
+struct Narrow {
+  static constexpr int T_BYTES = BKV * HD;
+  static constexpr int STAGES = 3;
+  static constexpr int PB = 4 * NR;  // bytes of a P row
+  static constexpr int P_BYTES = BKV * PB;
+  static constexpr int Q_BYTES = 2 * NR * HD;
+  static constexpr int TMEM = 8 * NR;
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * 2 * T_BYTES + P_BYTES + Q_BYTES + NR * 4 * 8 + 256;
+  static constexpr uint32_t IDESC_S = idesc_e4m3_f32(BKV, 2 * NR);
+  // A and B both M/N-major; the M = 128 lanes beyond a head of 64 are unused
+  static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(128, 4 * NR) | (1u << 15) | (1u << 16);
+  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024 || NR > 16, "two CTAs per SM");
+};
+
+// OR of a predicate over the named barrier's threads.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// 16-byte chunk c of P row r (rows of 64 or 128 bytes, swizzled over their width)
+template <int NR>
+__device__ __forceinline__ int p_swz(int r, int c) {
+  return NR == 16 ? swz<64>(r, c) : swz<128>(r, c);
+}
+
+template <int HD, int NR>
+__global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
+    narrow_kernel(const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p) {
+  using CF = Narrow<HD, NR>;
+  constexpr int ST = CF::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sK = smem;                        // ST tiles
+  uint8_t* sV = sK + ST * CF::T_BYTES;       // ST tiles (a head of 64 reads 512 bytes past one)
+  uint8_t* sP = sV + ST * CF::T_BYTES;       // [128 keys][p0 | p1 | p2 | 0]
+  uint8_t* sQ = sP + CF::P_BYTES;            // [NR hi rows][NR lo rows]
+  float* sF = reinterpret_cast<float*>(sQ + CF::Q_BYTES);  // [NR] row factors
+  float* sM = sF + NR;                                     // [NR] running maxima (log2 units)
+  int* sSees = reinterpret_cast<int*>(sM + NR);            // [NR] visible keys
+  float* sRed = reinterpret_cast<float*>(sSees + NR);      // [4][NR]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRed + 5 * NR);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = q_full + 1;       // [ST]
+  uint64_t* k_empty = k_full + ST;     // [ST]
+  uint64_t* v_full = k_empty + ST;     // [ST]
+  uint64_t* v_empty = v_full + ST;     // [ST]
+  uint64_t* s_full = v_empty + ST;     // [2]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 1;
+  uint64_t* drain = pv_done + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = warp_id();
+  const int lane = lane_id();
+  griddep_wait();
+  const Batch& bt = p.bt;
+  const int g = static_cast<int>(blockIdx.x) % p.Hkv;
+  const int b = static_cast<int>(blockIdx.x) / p.Hkv;
+  const int split = blockIdx.y;
+  const Seq s = load_seq(bt, b, p.max_prefix, 0x511, threadIdx.x == 0 && split == 0 && g == 0);
+  const int rows = s.n * p.group;
+  if (rows == 0) return;
+  const int total = s.c0 + s.n;
+  const int tiles = (total + BKV - 1) / BKV;
+  const int t_beg = split * p.tiles_per_split;
+  const int n = min(tiles, t_beg + p.tiles_per_split) - t_beg;
+  if (n <= 0) return;
+  const int log_ppt = 7 - bt.log_page;
+  const int pages = (total + bt.page - 1) >> bt.log_page;  // of the sequence
+  const int32_t* table = bt.page_table + static_cast<size_t>(b) * bt.max_pages;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, 128);
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, CF::TMEM);
+    tmem_relinquish();
+  }
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + NR) {
+    const int r = static_cast<int>(threadIdx.x) - 64;
+    sM[r] = -INFINITY;
+    sSees[r] = p.causal ? min(total, s.c0 + r / p.group + 1) : total;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch();  // only now: a successor's CTA must not take the TMEM before this one
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int ppt = 1 << log_ppt;
+    const int page_bytes = bt.page * HD;
+    int issued_k = 0, issued_v = 0;
+    int next = -1;  // page id of the next tile, loaded one tile ahead
+    if (lane < ppt && (t_beg << log_ppt) + lane < pages) next = table[(t_beg << log_ppt) + lane];
+    for (int j = 0; j < n; ++j) {
+      const int st = j % ST;
+      const int base = (t_beg + j) << log_ppt;
+      const int here = min(ppt, pages - base);
+      int pg = next;
+      if (j + 1 < n && lane < ppt && base + ppt + lane < pages) next = table[base + ppt + lane];
+      const int y = (pg < 0 || pg >= bt.n_pages) ? bt.n_pages * p.Hkv * bt.page
+                                                 : (pg * p.Hkv + g) * bt.page;
+      bool ok = j < ST || mbar_wait(&k_empty[st], ((j / ST) - 1) & 1, abort_flag, 0x561);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_expect_tx(&k_full[st], here * page_bytes);
+      __syncwarp();
+      if (lane < here)
+        tma_load_2d(sK + st * CF::T_BYTES + lane * page_bytes, &tm_k, &k_full[st], 0, y);
+      issued_k = j + 1;
+      ok = j < ST || mbar_wait(&v_empty[st], ((j / ST) - 1) & 1, abort_flag, 0x562);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_expect_tx(&v_full[st], here * page_bytes);
+      __syncwarp();
+      if (lane < here)
+        tma_load_2d(sV + st * CF::T_BYTES + lane * page_bytes, &tm_v, &v_full[st], 0, y);
+      issued_v = j + 1;
+    }
+    if (*abort_flag && lane == 0) {
+      for (int j = max(0, issued_k - ST); j < issued_k; ++j)
+        mbar_wait(&k_full[j % ST], (j / ST) & 1, nullptr, 0x563);
+      for (int j = max(0, issued_v - ST); j < issued_v; ++j)
+        mbar_wait(&v_full[j % ST], (j / ST) & 1, nullptr, 0x564);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = mbar_wait(q_full, 0, abort_flag, 0x571);
+      const uint32_t q_base = smem_u32(sQ), p_base = smem_u32(sP);
+      auto issue_s = [&](int j) -> bool {
+        const int st = j % ST;
+        if (!mbar_wait(&k_full[st], (j / ST) & 1, abort_flag, 0x572)) return false;
+        tc_fence_after();
+        const uint32_t k_base = smem_u32(sK + st * CF::T_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < HD / 32; ++kk)
+          umma_ss_f8(tmem + (j & 1) * 2 * NR, sdesc_rows<HD>(k_base + kk * 32),
+                     sdesc_rows<HD>(q_base + kk * 32), CF::IDESC_S, kk ? 1u : 0u);
+        umma_commit(&s_full[j & 1]);
+        umma_commit(&k_empty[st]);
+        return true;
+      };
+      if (ok) ok = issue_s(0);
+      if (ok && n > 1) ok = issue_s(1);
+      for (int j = 0; ok && j < n; ++j) {
+        const int st = j % ST;
+        ok = mbar_wait(&v_full[st], (j / ST) & 1, abort_flag, 0x573);
+        if (ok) ok = mbar_wait(p_full, j & 1, abort_flag, 0x574);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v_base = smem_u32(sV + st * CF::T_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < BKV / 32; ++kk) {
+          // 32 keys: four 8-row groups of V and of P
+          const uint64_t da = HD == 128 ? sdesc_sw128(v_base + kk * 32 * 128, 1024, 1024)
+                                        : sdesc_sw64(v_base + kk * 32 * 64, 512, 512);
+          const uint64_t db = NR == 16 ? sdesc_sw64(p_base + kk * 32 * 64, 512, 512)
+                                       : sdesc_sw128(p_base + kk * 32 * 128, 1024, 1024);
+          umma_ss_f8(tmem + 4 * NR, da, db, CF::IDESC_PV, (j | kk) ? 1u : 0u);
+        }
+        umma_commit(pv_done);
+        umma_commit(&v_empty[st]);
+        if (j + 2 < n) ok = issue_s(j + 2);
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, 0x575);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3;
+    const int kl = quarter * 32 + lane;  // key of the tile; later element of the head
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    load_q_rows<HD>(p, s, g, 0, rows, sQ, sQ + NR * HD, sF, (warp - 2) * (NR / 4), NR / 4);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    // the unused fourth of every P row
+#pragma unroll
+    for (int c = 0; c < NR / 16; ++c)
+      *reinterpret_cast<uint4*>(sP + p_swz<NR>(kl, 3 * (NR / 16) + c)) =
+          make_uint4(0u, 0u, 0u, 0u);
+    // page scales of this thread's key, one tile ahead
+    auto page_id = [&](int j) -> int {
+      const int at = ((t_beg + j) << log_ppt) + (kl >> bt.log_page);
+      return j < n && at < pages ? table[at] : -1;
+    };
+    auto page_exps = [&](int pg, int* ke, int* ve) {
+      *ke = *ve = 127;
+      if (pg >= 0 && pg < bt.n_pages) {
+        const size_t at = static_cast<size_t>(pg) * p.Hkv + g;
+        *ke = p.k_exp[at];
+        *ve = p.v_exp[at];
+      }
+    };
+    auto check_page = [&](int j, int pg) {
+      if ((pg < 0 || pg >= bt.n_pages) && (kl & (bt.page - 1)) == 0 &&
+          ((t_beg + j) << log_ppt) + (kl >> bt.log_page) < pages)
+        raise_error(ERR_CHECK | 0x512, static_cast<uint32_t>(b));
+    };
+    int ke, ve;
+    int pg = page_id(0);
+    page_exps(pg, &ke, &ve);
+    check_page(0, pg);
+    pg = page_id(1);
+    const int open_keys = p.causal ? s.c0 + 1 : total;  // keys below are visible to every row
+    float l[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) l[r] = 0.f;
+    bar_any(1, 128, false);  // row factors are in place
+    bool ok = true;
+    int j = 0;
+    for (; j < n; ++j) {
+      const float kf = __uint_as_float(static_cast<uint32_t>(ke) << 23);
+      const float ev = static_cast<float>(ve - 127);
+      const float l_scale = __uint_as_float(static_cast<uint32_t>(254 - ve) << 23);  // 2^-ev
+      if (j + 1 < n) {
+        page_exps(pg, &ke, &ve);
+        check_page(j + 1, pg);
+        pg = page_id(j + 2);
+      }
+      const int pos = (t_beg + j) * BKV + kl;
+      const bool edge = (t_beg + j + 1) * BKV > open_keys;
+      const uint32_t tS = tl + (j & 1) * 2 * NR;
+      ok = __all_sync(0xffffffffu,
+                      ok && mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag, 0x581));
+      tc_fence_after();
+      float x[NR];
+      // x = score in log2 units + shift - (with_max ? running maximum : 0)
+      auto scores = [&](float shift, bool with_max) {
+#pragma unroll
+        for (int c = 0; c < NR; c += 16) {
+          uint32_t hi[16], lo[16];
+          tmem_ld16(tS + c, hi);
+          tmem_ld16(tS + NR + c, lo);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 16; q += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sF + c + q);
+            const float4 m = *reinterpret_cast<const float4*>(sM + c + q);
+            const float ff[4] = {f.x, f.y, f.z, f.w}, mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float sum = __uint_as_float(hi[q + e]) + __uint_as_float(lo[q + e]);
+              x[c + q + e] = fmaf(sum, ff[e] * kf, with_max ? shift - mm[e] : shift);
+              if (edge && pos >= sSees[c + q + e]) x[c + q + e] = -INFINITY;
+            }
+          }
+        }
+      };
+      scores(ev + N_SHIFT, true);
+      bool above = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) above = above || x[r] > N_LIMIT;
+      if (bar_any(1, 128, above || !ok)) {
+        if (bar_any(1, 128, !ok || *abort_flag)) break;
+        // raise the maxima to this tile's
+        scores(ev, false);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          float v = x[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          if (lane == 0) sRed[quarter * NR + r] = v;
+        }
+        if (j > 0) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (j - 1) & 1, abort_flag, 0x582));
+          tc_fence_after();
+        }
+        bar_any(1, 128, false);
+        float mine = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NR; c += 16) {
+          float fac[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = c + e;
+            const float old = sM[r];
+            const float top = fmaxf(fmaxf(fmaxf(sRed[r], sRed[NR + r]),
+                                          fmaxf(sRed[2 * NR + r], sRed[3 * NR + r])), old);
+            fac[e] = old == -INFINITY ? 0.f : attn::fast_exp2(old - top);
+            l[r] *= fac[e];
+            if (r == kl) mine = top;
+          }
+          if (j > 0) {
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              uint32_t o[16];
+              tmem_ld16(tl + 4 * NR + term * NR + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * fac[e]);
+              tmem_st16(tl + 4 * NR + term * NR + c, o);
+            }
+          }
+        }
+        tmem_st_wait();
+        bar_any(1, 128, false);  // everyone has read the old maxima
+        if (kl < NR) sM[kl] = mine;
+        bar_any(1, 128, false);
+        scores(ev + N_SHIFT, true);
+      }
+      // P rows may be rewritten once the previous product has read them
+      if (j > 0)
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (j - 1) & 1, abort_flag, 0x583));
+#pragma unroll
+      for (int c = 0; c < NR; c += 16) {
+        uint32_t w[3][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t term[3][2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = c + 4 * q + 2 * e;
+            const float p0 = attn::fast_exp2(x[r]), p1 = attn::fast_exp2(x[r + 1]);
+            l[r] = fmaf(p0, l_scale, l[r]);
+            l[r + 1] = fmaf(p1, l_scale, l[r + 1]);
+            __half2 rest = __floats2half2_rn(p0, p1);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              const __nv_fp8x2_storage_t code =
+                  __nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E4M3);
+              term[t][e] = code;
+              if (t < 2)
+                rest = __hmul2(__hsub2(rest, __half2(__nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3))),
+                               __float2half2_rn(16.f));
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 3; ++t) w[t][q] = term[t][0] | (term[t][1] << 16);
+        }
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          *reinterpret_cast<uint4*>(sP + p_swz<NR>(kl, t * (NR / 16) + c / 16)) =
+              make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+      }
+      if (pos >= total) {
+        // whatever lies behind the sequence's end must not meet the product
+        const int st = j % ST;
+        ok = mbar_wait(&v_full[st], (j / ST) & 1, abort_flag, 0x584) && ok;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c)
+          reinterpret_cast<uint4*>(sV + st * CF::T_BYTES + kl * HD)[c] =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(p_full);
+    }
+    // ------------------------------------------------------------ results
+    ok = __all_sync(0xffffffffu, ok && j == n &&
+                                     mbar_wait(pv_done, (n - 1) & 1, abort_flag, 0x585));
+    tc_fence_after();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float v = warp_sum(l[r]);
+      if (lane == 0) sRed[quarter * NR + r] = v;
+    }
+    bar_any(1, 128, false);
+    const size_t part = static_cast<size_t>(split) * bt.T * p.Hq;
+    if (ok && kl < rows) {
+      const float sum = (sRed[kl] + sRed[NR + kl]) + (sRed[2 * NR + kl] + sRed[3 * NR + kl]);
+      const int tok = kl / p.group;
+      const size_t at = static_cast<size_t>(s.t0 + tok) * p.Hq + g * p.group + kl - tok * p.group;
+      const float z = sum == 0.f ? -INFINITY
+                                 : (sM[kl] - N_SHIFT + log2f(sum)) * 0.69314718055994531f;
+      if (p.n_splits > 1)
+        p.part_lse[part + at] = z;
+      else if (p.lse)
+        p.lse[at] = z;
+    }
+    int tok = 0, hh = 0;
+#pragma unroll
+    for (int c = 0; c < NR; c += 16) {
+      if (c >= rows) break;
+      uint32_t o0[16], o1[16], o2[16];
+      tmem_ld16(tl + 4 * NR + c, o0);
+      tmem_ld16(tl + 5 * NR + c, o1);
+      tmem_ld16(tl + 6 * NR + c, o2);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int r = c + e;
+        if (r < rows && ok && kl < HD) {
+          const float sum = (sRed[r] + sRed[NR + r]) + (sRed[2 * NR + r] + sRed[3 * NR + r]);
+          const float v = fmaf(__uint_as_float(o2[e]), 1.f / 256.f,
+                               fmaf(__uint_as_float(o1[e]), 1.f / 16.f, __uint_as_float(o0[e]))) *
+                          (sum == 0.f ? 0.f : 1.f / sum);
+          const int h = g * p.group + hh;
+          if (p.n_splits > 1)
+            p.part_o[(part + static_cast<size_t>(s.t0 + tok) * p.Hq + h) * HD + kl] = v;
+          else
+            p.out[static_cast<size_t>(s.t0 + tok) * p.ldo + static_cast<size_t>(h) * HD + kl] =
+                __float2bfloat16_rn(v);
+        }
+        if (++hh == p.group) {
+          hh = 0;
+          ++tok;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, CF::TMEM);
   }
 }
 
