@@ -709,10 +709,8 @@ PagedPlan plan_paged(int B, int Hq, int Hkv, int max_new, long long max_keys) {
     pl.rows = rows <= 16 ? 16 : 32;
     pl.n_pairs = 1;
     const long long units = (long long)B * Hkv;
-    static const int slots = getenv("DG_NSLOTS") ? atoi(getenv("DG_NSLOTS")) : 2 * kNumSMs;
-    static const int most = getenv("DG_NMOST") ? atoi(getenv("DG_NMOST")) : 16;
-    const long long even = (units * tiles + slots - 1) / slots;
-    const int per = (int)std::min<long long>(std::max(1ll, even), most);
+    const long long even = (units * tiles + 2 * kNumSMs - 1) / (2 * kNumSMs);
+    const int per = (int)std::min<long long>(std::max(1ll, even), 64);
     pl.tiles_per_split = cdiv(tiles, cdiv(tiles, per));
     pl.n_splits = cdiv(tiles, pl.tiles_per_split);
     return pl;
@@ -1768,6 +1766,9 @@ int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uin
   dg::paged::AttnParams p;
   p.bt = {B, T, max_new, max_pages, page, log2_of(page), n_pages, tok_start, cache_len, page_table};
   p.Hq = Hq; p.Hkv = Hkv; p.group = Hq / Hkv;
+  p.group_shift = 0;
+  while ((1ll << p.group_shift) < p.group) ++p.group_shift;
+  p.group_mul = p.group == 1 ? 0u : (uint32_t)((1ull << (31 + p.group_shift)) / p.group + 1);
   p.causal = mask_mode == DG_MASK_CAUSAL ? 1 : 0;
   p.max_prefix = max_prefix;
   p.n_pairs = pl.n_pairs;

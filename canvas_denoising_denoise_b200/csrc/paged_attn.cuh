@@ -73,6 +73,7 @@ __device__ __forceinline__ int swz(int r, int c) {
 struct AttnParams {
   Batch bt;
   int Hq, Hkv, group, causal;
+  uint32_t group_mul, group_shift;  // token_of()
   int max_prefix;
   int n_pairs;           // query-row blocks (of 256 packed rows) per kv head
   int tiles_per_split;   // key tiles per CTA
@@ -88,72 +89,99 @@ struct AttnParams {
   float* part_lse;  // [n_splits, T, Hq]
 };
 
-// Two e4m3 values whose sum is a scaled query element.
-__device__ __forceinline__ void split_q(const float (&x)[8], float f, uint2* hi, uint2* lo) {
-  float h[8], r[8];
-  *hi = pack_e4m3x8(x, f);
-  unpack_e4m3x8(*hi, h);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = fmaf(x[e], f, -h[e]);
-  *lo = pack_e4m3x8(r, 1.f);
+// Token of a packed row below 2^31: row / group by a multiplication.  With s =
+// ceil(log2 group) and mul = floor(2^(31 + s) / group) + 1 < 2^32 the error
+// row (mul - 2^(31 + s) / group) / 2^(31 + s) stays below 1 / group.
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) {
+  return p.group == 1 ? row
+                      : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_mul) >>
+                                         (p.group_shift - 1));
 }
 
-// A warp converts rows [r0, r0 + n_rows) of a tile of packed query rows (first row
-// `first` of `rows` in the kv head's group) to hi / lo tiles, and stores each
-// row's factor scale_log2 * 2^e.  A row that holds an infinity or a NaN gets a
-// NaN factor, so that its scores are NaN; rows past the end are zero.
-template <int HD>
+// Eight scaled query elements as e4m3 hi + lo.  x f (f a power of two) fits f16
+// exactly down to 2^-17, far below what lo can still hold (2^-10).
+__device__ __forceinline__ void split_q(uint4 raw, float f, uint2* hi, uint2* lo) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t h[4], r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * f,
+                                        __uint_as_float(w[i] & 0xFFFF0000u) * f);
+    h[i] = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 back = __half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[i]), __NV_E4M3));
+    r[i] = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(__hsub2(x, back)), __NV_SATFINITE, __NV_E4M3);
+  }
+  *hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  *lo = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+
+// 16 bytes global -> shared, asynchronously; zeros when !valid (src is not read).
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+
+// A warp brings rows [r0, r0 + ROWS) of a tile of packed query rows (first row
+// `first` of `rows` in the kv head's group) into shared memory as hi / lo
+// tiles, and stores each row's factor scale_log2 * 2^e.  A row that holds an
+// infinity or a NaN gets a NaN factor, so that its scores are NaN; rows past
+// the end are zero.  The bf16 row first lands, all rows in flight together, in
+// the bytes that its two halves will take: its 16-byte chunk c in chunk
+// c % (hd / 16) of hi, then of lo.  Both loops stay rolled: this code runs
+// once per CTA, and unrolled it waits for instruction fetches (8 us, of which
+// 2 us remain).
+template <int HD, int ROWS>
 __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, int g, int first,
                                             int rows, uint8_t* hi, uint8_t* lo, float* factor,
-                                            int r0, int n_rows) {
-  constexpr int LANES = HD / 8;        // lanes per row
-  constexpr int PER = 32 / LANES;      // rows per pass
-  constexpr int BATCH = 4;             // passes whose loads are in flight together
+                                            int r0) {
+  constexpr int LANES = HD / 8;                   // lanes per row
+  constexpr int PER = 32 / LANES;                 // rows per pass
+  constexpr int PASSES = (ROWS + PER - 1) / PER;
   const int lane = lane_id();
   const int c8 = lane % LANES;
-  for (int rb = 0; rb < n_rows; rb += PER * BATCH) {
-    uint4 raw[BATCH];
+  uint8_t* raw = c8 < HD / 16 ? hi : lo;
+#pragma unroll 2
+  for (int u = 0; u < PASSES; ++u) {
+    const int i = u * PER + lane / LANES;
+    const int pr = first + r0 + i;
+    const int tok = token_of(p, pr);
+    const bool valid = pr < rows;
+    const __nv_bfloat16* src =
+        p.q + (valid ? static_cast<size_t>(s.t0 + tok) * p.ldq +
+                           static_cast<size_t>(g * p.group + pr - tok * p.group) * HD + c8 * 8
+                     : 0);
+    if (i < ROWS) copy16_async(raw + swz<HD>(r0 + i, c8 % (HD / 16)), src, valid);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+#pragma unroll 2
+  for (int u = 0; u < PASSES; ++u) {
+    const int i = u * PER + lane / LANES;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (i < ROWS)
+      x = *reinterpret_cast<const uint4*>(raw + swz<HD>(r0 + i, c8 % (HD / 16)));
+    // largest magnitude of the row as bf16 bits (an integer order in which
+    // infinities and NaN come last)
+    uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                            __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int r = r0 + rb + u * PER + lane / LANES;
-      const int pr = first + r;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (pr < rows && r < r0 + n_rows) {
-        const int tok = pr / p.group;
-        raw[u] = *reinterpret_cast<const uint4*>(
-            p.q + static_cast<size_t>(s.t0 + tok) * p.ldq +
-            static_cast<size_t>(g * p.group + pr - tok * p.group) * HD + c8 * 8);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int r = r0 + rb + u * PER + lane / LANES;
-      float x[8];
-      unpack_bf16x8(raw[u], x);
-      float amax = 0.f;
-      bool fine = true;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = fabsf(x[e]);
-        fine = fine && v <= FLT_MAX;
-        amax = fmaxf(amax, v);
-      }
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const uint32_t bad = __ballot_sync(0xffffffffu, !fine);
-      const bool row_fine = ((bad >> (lane & ~(LANES - 1))) & ((1ull << LANES) - 1)) == 0;
-      // 2^e with amax <= 448 2^e; a row of zeros takes e = -100
-      const uint32_t bits = __float_as_uint(amax);
-      const int e = max(static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u), -100);
-      uint2 vh = make_uint2(0u, 0u), vl = make_uint2(0u, 0u);
-      if (row_fine) split_q(x, pow2(-min(e, 126)), &vh, &vl);
-      if (r >= r0 + n_rows) continue;
+    for (int o = LANES / 2; o > 0; o >>= 1)
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = max(top & 0xFFFFu, top >> 16);
+    const bool fine = top < 0x7F80u;
+    // the smallest e with amax <= 448 2^e = 1.75 2^(e + 8), at least -100
+    const int e = max(static_cast<int>(top >> 7) - 135 + ((top & 0x7Fu) > 0x60u ? 1 : 0), -100);
+    uint2 vh = make_uint2(0u, 0u), vl = make_uint2(0u, 0u);
+    if (fine) split_q(x, pow2(-e), &vh, &vl);
+    __syncwarp();  // the row has been read
+    if (i < ROWS) {
+      const int r = r0 + i;
       const int at = swz<HD>(r, c8 >> 1) + (c8 & 1) * 8;
       *reinterpret_cast<uint2*>(hi + at) = vh;
       *reinterpret_cast<uint2*>(lo + at) = vl;
-      if (c8 == 0)
-        factor[r] = row_fine ? p.scale_log2 * pow2(min(e, 126)) : __int_as_float(0x7FC00000);
+      if (c8 == 0) factor[r] = fine ? p.scale_log2 * pow2(e) : __int_as_float(0x7FC00000);
     }
   }
 }
@@ -161,10 +189,15 @@ __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, i
 // ---------------------------------------------------------------------------
 // Many query rows per kv head: two 128-row query tiles per CTA
 // ---------------------------------------------------------------------------
-// Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer, 2..5 / 6..9 = softmax
-// of tile A / B (one query row per thread), 10..13 = V expansion (codes ->
-// f16 tiles in shared memory, rows past the sequence's end zeroed).
-constexpr int WIDE_THREADS = 448;
+// Four warpgroups, with registers moved to the softmax (setmaxnreg):
+//   warps 0..3    0 = TMA producer, 1 = TMEM owner + MMA issuer (40 registers)
+//   warps 4..11   softmax of tile A / B, one query row per thread (192)
+//   warps 12..15  V expansion: codes -> f16 tiles in shared memory, rows past
+//                 the visible keys zeroed (88)
+// A softmax thread holds its 128 scores in registers between the maximum and
+// the exponentials, and hands P over in two halves of 64 keys, so that P V
+// starts while the second half is still being formed.
+constexpr int WIDE_THREADS = 512;
 constexpr float P_SHIFT = 7.f;  // probabilities are held as 2^(s - m + 7): at most 2^15 in f16
 constexpr int V_SHIFT = 7;      // V codes as code 2^(ev - emax + 7): at most 57344 in f16
 
@@ -175,11 +208,12 @@ struct Wide {
   static constexpr int KST = 3, VST = 2, HST = 2;  // stages of K codes, V codes, V f16
   static constexpr int RING = KST * T_BYTES + VST * T_BYTES + HST * V16_BYTES;
   static constexpr int MAX_PAGES = MAX_TILES * (BKV / 16);
-  static constexpr int SMEM_BYTES = 1024 + 4 * T_BYTES + RING + MAX_PAGES * 9 + 2 * BQ * 4 + 512;
+  static constexpr int SMEM_BYTES = 1024 + 4 * T_BYTES + RING + MAX_PAGES * 5 + 2 * BQ * 4 + 512;
   static constexpr uint32_t IDESC_S = idesc_e4m3_f32(BQ, BKV);
   static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(BQ, HD);
   static_assert(RING >= 2 * BQ * HD * 4, "O staging does not fit the rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  static_assert(40 + 2 * 192 + 88 == 512, "register shares exceed the launch's 128 a thread");
 };
 
 template <int HD>
@@ -196,30 +230,35 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   uint8_t* sV8 = sK + CF::KST * CF::T_BYTES;       // VST tiles, plain rows
   float* sQf = reinterpret_cast<float*>(sV8 + CF::VST * CF::T_BYTES);  // [256] row factors
   float* sKf = sQf + 2 * BQ;                                           // [MAX_PAGES] 2^ek
-  int* sPage = reinterpret_cast<int*>(sKf + CF::MAX_PAGES);            // [MAX_PAGES]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sPage + CF::MAX_PAGES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKf + CF::MAX_PAGES);
   uint64_t* q_full = bars;
-  uint64_t* k_full = q_full + 1;              // [KST]
+  uint64_t* meta_full = q_full + 1;           // page scales are in shared memory
+  uint64_t* k_full = meta_full + 1;           // [KST]
   uint64_t* k_empty = k_full + CF::KST;       // [KST]
   uint64_t* v8_full = k_empty + CF::KST;      // [VST]
   uint64_t* v8_empty = v8_full + CF::VST;     // [VST]
   uint64_t* v16_full = v8_empty + CF::VST;    // [HST]
   uint64_t* v16_empty = v16_full + CF::HST;   // [HST]
   uint64_t* s_full = v16_empty + CF::HST;     // [2] per query tile
-  uint64_t* p_full = s_full + 2;              // [2]
-  uint64_t* o_final = p_full + 2;
+  uint64_t* p_full = s_full + 2;              // [2 tiles][2 halves]
+  uint64_t* o_final = p_full + 4;
   uint64_t* drain = o_final + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_emax = reinterpret_cast<int*>(tmem_holder + 2);
-  uint8_t* sVe = reinterpret_cast<uint8_t*>(tmem_holder + 4);  // [MAX_PAGES] biased ev
+  int* s_emax = reinterpret_cast<int*>(tmem_holder + 2);       // [4]
+  uint8_t* sVe = reinterpret_cast<uint8_t*>(tmem_holder + 8);  // [MAX_PAGES] biased ev
 
   const int warp = warp_id();
   const int lane = lane_id();
   griddep_wait();
   const Batch& bt = p.bt;
-  const int pi = static_cast<int>(blockIdx.x) % p.n_pairs;
-  const int gb = static_cast<int>(blockIdx.x) / p.n_pairs;
+  // Causal launches take their heaviest row blocks (the last) first, so that
+  // the light ones fill the tail of the grid.
+  const int nbg = p.Hkv * bt.B;
+  const int pi = p.causal ? p.n_pairs - 1 - static_cast<int>(blockIdx.x) / nbg
+                          : static_cast<int>(blockIdx.x) % p.n_pairs;
+  const int gb = p.causal ? static_cast<int>(blockIdx.x) % nbg
+                          : static_cast<int>(blockIdx.x) / p.n_pairs;
   const int g = gb % p.Hkv;
   const int b = gb / p.Hkv;
   const int split = blockIdx.y;
@@ -230,7 +269,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   if (first >= rows) return;
   const bool vB = first + BQ < rows;
   const int total = s.c0 + s.n;
-  const int last_tok = (min(rows, first + 2 * BQ) - 1) / p.group;
+  const int last_tok = token_of(p, min(rows, first + 2 * BQ) - 1);
   const int visible = p.causal ? s.c0 + last_tok + 1 : total;  // keys that this CTA's rows see
   const int tiles = (visible + BKV - 1) / BKV;
   const int t_beg = split * p.tiles_per_split;
@@ -239,9 +278,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   const int log_ppt = 7 - bt.log_page;  // log2(pages per tile)
   const int page_beg = t_beg << log_ppt;
   const int n_pages = ((min(visible, (t_beg + n) * BKV) + bt.page - 1) >> bt.log_page) - page_beg;
+  const int32_t* table = bt.page_table + static_cast<size_t>(b) * bt.max_pages + page_beg;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, vB ? 8 : 4);
+    mbar_init(meta_full, 4);
     for (int i = 0; i < CF::KST; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -254,95 +295,71 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       mbar_init(&v16_full[i], 4);
       mbar_init(&v16_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], BQ);
-    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], BQ);
     mbar_init(o_final, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *s_emax = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
-  // page ids and scales of the whole key range
-  int emax = 0;
-  for (int i = threadIdx.x; i < (n << log_ppt); i += WIDE_THREADS) {
-    int pg = -1;
-    float kf = 1.f;
-    int ve = 0;
-    if (i < n_pages) {
-      pg = bt.page_table[static_cast<size_t>(b) * bt.max_pages + page_beg + i];
-      if (pg < 0 || pg >= bt.n_pages) {
-        raise_error(ERR_CHECK | 0x512, static_cast<uint32_t>(b));
-        pg = -1;
-      } else {
-        const size_t at = static_cast<size_t>(pg) * p.Hkv + g;
-        kf = __uint_as_float(static_cast<uint32_t>(p.k_exp[at]) << 23);
-        ve = p.v_exp[at];
-      }
-    }
-    sPage[i] = pg;
-    sKf[i] = kf;
-    sVe[i] = static_cast<uint8_t>(ve);
-    emax = max(emax, ve);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   griddep_launch();  // only now: a successor's CTA must not take the TMEM before this one
-  emax = __reduce_max_sync(0xffffffffu, emax);
-  if (lane == 0 && emax > 0) atomicMax(s_emax, emax);
-  __syncthreads();
-  emax = *s_emax;
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    // Lane l loads page l of the tile.  A page outside the table's range was
-    // reported above; it is read as zeros (a box past the tensor's end).
-    const int ppt = 1 << log_ppt;
-    const int page_bytes = bt.page * HD;
-    int issued = 0;
-    for (int j = 0; j < n; ++j) {
-      const int ks = j % CF::KST, vs = j % CF::VST;
-      bool ok = j < CF::KST || mbar_wait(&k_empty[ks], ((j / CF::KST) - 1) & 1, abort_flag, 0x521);
-      ok = ok && (j < CF::VST ||
-                  mbar_wait(&v8_empty[vs], ((j / CF::VST) - 1) & 1, abort_flag, 0x522));
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int pages = min(ppt, n_pages - (j << log_ppt));
-      if (lane == 0) {
-        mbar_expect_tx(&k_full[ks], pages * page_bytes);
-        mbar_expect_tx(&v8_full[vs], pages * page_bytes);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      // Lane l loads page l of the tile.  A page outside the pool is reported
+      // by the V expansion and read as zeros (a box past the tensor's end).
+      const int ppt = 1 << log_ppt;
+      const int page_bytes = bt.page * HD;
+      int issued = 0;
+      int next = lane < min(ppt, n_pages) ? table[lane] : -1;  // one tile ahead
+      for (int j = 0; j < n; ++j) {
+        const int ks = j % CF::KST, vs = j % CF::VST;
+        const int pages = min(ppt, n_pages - (j << log_ppt));
+        const int pg = next;
+        if (lane < ppt && ((j + 1) << log_ppt) + lane < n_pages)
+          next = table[((j + 1) << log_ppt) + lane];
+        bool ok =
+            j < CF::KST || mbar_wait(&k_empty[ks], ((j / CF::KST) - 1) & 1, abort_flag, 0x521);
+        ok = ok && (j < CF::VST ||
+                    mbar_wait(&v8_empty[vs], ((j / CF::VST) - 1) & 1, abort_flag, 0x522));
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          mbar_expect_tx(&k_full[ks], pages * page_bytes);
+          mbar_expect_tx(&v8_full[vs], pages * page_bytes);
+        }
+        __syncwarp();
+        if (lane < pages) {
+          const int y = (pg < 0 || pg >= bt.n_pages) ? bt.n_pages * p.Hkv * bt.page
+                                                     : (pg * p.Hkv + g) * bt.page;
+          tma_load_2d(sK + ks * CF::T_BYTES + lane * page_bytes, &tm_k, &k_full[ks], 0, y);
+          tma_load_2d(sV8 + vs * CF::T_BYTES + lane * page_bytes, &tm_v, &v8_full[vs], 0, y);
+        }
+        issued = j + 1;
       }
-      __syncwarp();
-      if (lane < pages) {
-        const int pg = sPage[(j << log_ppt) + lane];
-        const int y = pg < 0 ? bt.n_pages * p.Hkv * bt.page : (pg * p.Hkv + g) * bt.page;
-        tma_load_2d(sK + ks * CF::T_BYTES + lane * page_bytes, &tm_k, &k_full[ks], 0, y);
-        tma_load_2d(sV8 + vs * CF::T_BYTES + lane * page_bytes, &tm_v, &v8_full[vs], 0, y);
+      if (*abort_flag && lane == 0) {
+        for (int j = max(0, issued - CF::KST); j < issued; ++j)
+          mbar_wait(&k_full[j % CF::KST], (j / CF::KST) & 1, nullptr, 0x523);
+        for (int j = max(0, issued - CF::VST); j < issued; ++j)
+          mbar_wait(&v8_full[j % CF::VST], (j / CF::VST) & 1, nullptr, 0x524);
       }
-      issued = j + 1;
-    }
-    if (*abort_flag && lane == 0) {
-      for (int j = max(0, issued - CF::KST); j < issued; ++j)
-        mbar_wait(&k_full[j % CF::KST], (j / CF::KST) & 1, nullptr, 0x523);
-      for (int j = max(0, issued - CF::VST); j < issued; ++j)
-        mbar_wait(&v8_full[j % CF::VST], (j / CF::VST) & 1, nullptr, 0x524);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
       bool ok = mbar_wait(q_full, 0, abort_flag, 0x531);
       const uint32_t q_base = smem_u32(sQ);
       auto issue_s = [&](int X, int j) {  // S_X = (hi + lo) K^T
         const uint32_t k_base = smem_u32(sK + (j % CF::KST) * CF::T_BYTES);
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < HD / 32; ++kk)
@@ -352,14 +369,19 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         umma_commit(&s_full[X]);
       };
       auto issue_pv = [&](int X, int j) -> bool {
-        if (!mbar_wait(&p_full[X], j & 1, abort_flag, 0x533)) return false;
-        tc_fence_after();
         const uint32_t v_base = smem_u32(sV16 + (j % CF::HST) * CF::V16_BYTES);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(&p_full[2 * X + half], j & 1, abort_flag, 0x533)) return false;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < BKV / 16; ++kk)
-          umma_ts(tmem + 256 + X * 128, tmem + X * 128 + kk * 8,
-                  sdesc_sw128(v_base + kk * 16 * 128, BKV * 128, 1024), CF::IDESC_PV,
-                  (j | kk) ? 1u : 0u);
+          for (int k4 = 0; k4 < BKV / 32; ++k4) {
+            const int kk = half * (BKV / 32) + k4;
+            umma_ts(tmem + 256 + X * 128, tmem + X * 128 + kk * 8,
+                    sdesc_sw128(v_base + kk * 16 * 128, BKV * 128, 1024), CF::IDESC_PV,
+                    (j | kk) ? 1u : 0u);
+          }
+        }
         return true;
       };
       if (ok) ok = mbar_wait(&k_full[0], 0, abort_flag, 0x532);
@@ -392,9 +414,34 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, 0x535);
     }
-  } else if (warp >= 10) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------ V expansion
-    const int tid = static_cast<int>(threadIdx.x) - 320;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const int tid = static_cast<int>(threadIdx.x) - 384;
+    // scales of the whole key range, and the largest V scale among them
+    int emax = 0;
+    for (int i = tid; i < (n << log_ppt); i += 128) {
+      float kf = 1.f;
+      int ve = 0;
+      if (i < n_pages) {
+        const int pg = table[i];
+        if (pg < 0 || pg >= bt.n_pages) {
+          raise_error(ERR_CHECK | 0x512, static_cast<uint32_t>(b));
+        } else {
+          const size_t at = static_cast<size_t>(pg) * p.Hkv + g;
+          kf = __uint_as_float(static_cast<uint32_t>(p.k_exp[at]) << 23);
+          ve = p.v_exp[at];
+        }
+      }
+      sKf[i] = kf;
+      sVe[i] = static_cast<uint8_t>(ve);
+      emax = max(emax, ve);
+    }
+    emax = __reduce_max_sync(0xffffffffu, emax);
+    if (lane == 0) s_emax[warp - 12] = emax;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    emax = max(max(s_emax[0], s_emax[1]), max(s_emax[2], s_emax[3]));
+    if (lane == 0) mbar_arrive(meta_full);
     constexpr int CPR = HD / 16;            // 16-code chunks per row
     constexpr int RSTEP = 128 / CPR;        // rows per pass
     constexpr int PASSES = BKV / RSTEP;
@@ -414,7 +461,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       const uint8_t* src = sV8 + vs * CF::T_BYTES;
       uint8_t* dst = sV16 + hs * CF::V16_BYTES + half_off;
       const int live = visible - (t_beg + j) * BKV;  // rows of this tile that were loaded
-#pragma unroll
+#pragma unroll 2
       for (int u = 0; u < PASSES; ++u) {
         const int r = r0 + u * RSTEP;
         uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
@@ -451,56 +498,58 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax (tile X)
-    const int X = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int X = (warp - 4) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const int qrow = first + X * BQ + r;  // packed row
-    const bool mine = X == 0 || vB;
-    if (mine) {
-      load_q_rows<HD>(p, s, g, first + X * BQ, rows, sQ + 2 * X * CF::T_BYTES,
-                      sQ + (2 * X + 1) * CF::T_BYTES, sQf + X * BQ, quarter * 32, 32);
+    bool ok = X == 0 || vB;
+    if (ok) {
+      load_q_rows<HD, 32>(p, s, g, first + X * BQ, rows, sQ + 2 * X * CF::T_BYTES,
+                          sQ + (2 * X + 1) * CF::T_BYTES, sQf + X * BQ, quarter * 32);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
+      ok = __all_sync(0xffffffffu, mbar_wait(meta_full, 0, abort_flag, 0x552));
     }
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + X * 128 + lane_off;
     const uint32_t tO = tmem + 256 + X * 128 + lane_off;
     float m = -INFINITY;  // running max in log2 units
     float l = 0.f;
-    bool ok = mine;
-    const float sc = mine ? sQf[X * BQ + r] : 0.f;
+    const float sc = ok ? sQf[X * BQ + r] : 0.f;
     // keys [0, sees) are visible to this row
-    const int sees = p.causal ? min(total, s.c0 + qrow / p.group + 1) : total;
+    const int sees = p.causal ? min(total, s.c0 + token_of(p, qrow) + 1) : total;
     for (int j = 0; j < n && ok; ++j) {
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[X], j & 1, abort_flag, 0x551))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int lim = sees - (t_beg + j) * BKV - 1;  // columns [0, lim] are visible
-      const bool masked = __any_sync(0xffffffffu, lim < BKV - 1);
+      uint32_t sa[128];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        tmem_ld32(tS + h * 32, *reinterpret_cast<uint32_t(*)[32]>(&sa[32 * h]));
       float scg[8];  // row factor times the page scale, per 16 columns
 #pragma unroll
       for (int q = 0; q < 8; ++q) scg[q] = sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)];
+      const int lim = sees - (t_beg + j) * BKV - 1;  // columns [0, lim] are visible
+      tmem_ld_wait();
+      if (__any_sync(0xffffffffu, lim < BKV - 1)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > lim) sa[c] = __float_as_uint(-INFINITY);
+      }
       float tmax = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t sa[32];
-        tmem_ld32(tS + h * 32, sa);
-        tmem_ld_wait();
-        if (masked) {
+      for (int q = 0; q < 8; ++q) {
+        float m0 = __uint_as_float(sa[16 * q]), m1 = __uint_as_float(sa[16 * q + 1]);
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (h * 32 + c > lim) sa[c] = __float_as_uint(-INFINITY);
+        for (int c = 2; c < 16; c += 2) {
+          m0 = fmaxf(m0, __uint_as_float(sa[16 * q + c]));
+          m1 = fmaxf(m1, __uint_as_float(sa[16 * q + c + 1]));
         }
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          m0 = fmaxf(m0, __uint_as_float(sa[c]));
-          m1 = fmaxf(m1, __uint_as_float(sa[16 + c]));
-        }
-        tmax = fmaxf(tmax, fmaxf(m0 * scg[2 * h], m1 * scg[2 * h + 1]));
+        tmax = fmaxf(tmax, fmaxf(m0, m1) * scg[q]);
       }
       // Raise the running max only when it grows by more than 2^8 (1/l keeps
       // this exact).  PV_X(j-1) is complete because S_X(j) is.
@@ -509,107 +558,97 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const float m_new = fmaxf(tmax, m);
         if (j > 0) {
           const float f = (m == -INFINITY) ? 0.f : attn::fast_exp2(m - m_new);
-#pragma unroll
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + c * 16, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tO + c * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(tO + c * 16, o);
           }
           l *= f;
         }
         m = m_new;
       }
       const float neg_m = (m == -INFINITY) ? 0.f : P_SHIFT - m;
-      float rs0 = 0.f, rs1 = 0.f, rs2 = 0.f, rs3 = 0.f;
+      float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        uint32_t sa[32];
-        tmem_ld32(tS + h * 32, sa);
-        tmem_ld_wait();
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (h * 32 + c > lim) sa[c] = __float_as_uint(-INFINITY);
-        }
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
+        for (int c = 0; c < 16; ++c) {
           const float f = scg[2 * h + (c >> 3)];
-          const float p0 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c]), f, neg_m));
-          const float p1 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c + 1]), f, neg_m));
-          const float p2 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c + 2]), f, neg_m));
-          const float p3 = attn::fast_exp2(fmaf(__uint_as_float(sa[2 * c + 3]), f, neg_m));
-          rs0 += p0;
-          rs1 += p1;
-          rs2 += p2;
-          rs3 += p3;
-          const __half2 a = __floats2half2_rn(p0, p1), d = __floats2half2_rn(p2, p3);
+          const float p0 = attn::fast_exp2(fmaf(__uint_as_float(sa[32 * h + 2 * c]), f, neg_m));
+          const float p1 = attn::fast_exp2(fmaf(__uint_as_float(sa[32 * h + 2 * c + 1]), f, neg_m));
+          rs[(2 * c) & 3] += p0;
+          rs[(2 * c + 1) & 3] += p1;
+          const __half2 a = __floats2half2_rn(p0, p1);
           pk[c] = *reinterpret_cast<const uint32_t*>(&a);
-          pk[c + 1] = *reinterpret_cast<const uint32_t*>(&d);
         }
-        // P overwrites S: 32 scores become 16 columns, always behind the reads
-        tmem_st16(tS + h * 16, pk);
+        tmem_st16(tS + h * 16, pk);  // P takes the first half of S's columns
+        if (h & 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * X + (h >> 1)]);
+        }
       }
-      l += (rs0 + rs1) + (rs2 + rs3);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&p_full[X]);
+      l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
     }
     const bool fin = __all_sync(0xffffffffu, ok && mbar_wait(o_final, 0, abort_flag, 0x553));
     // Stage O_X in the idle rings (rows XOR-swizzled by 16-byte chunk), then
     // write whole rows: coalesced stores, fp32 partials or bf16 results.
-    float* stage = reinterpret_cast<float*>(sV16) + X * (BQ * HD);
-    const int tok_r = qrow / p.group;
-    const int h_r = g * p.group + qrow - tok_r * p.group;
-    // probabilities carry 2^P_SHIFT in O and in l alike; V carries 2^(V_SHIFT - emax)
-    const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(emax - 127 - V_SHIFT)) / l;
-    const float lse_nat =
-        l == 0.f ? -INFINITY : (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
     if (fin) {
-      tc_fence_after();
+      float* stage = reinterpret_cast<float*>(sV16) + X * (BQ * HD);
+      int emax = 0;
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + c * 32, o);
+      for (int i = 0; i < 4; ++i) emax = max(emax, s_emax[i]);
+      // probabilities carry 2^P_SHIFT in O and in l alike; V carries 2^(V_SHIFT - emax)
+      const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(emax - 127 - V_SHIFT)) / l;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < HD / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
         tmem_ld_wait();
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const int chunk = (c * 8 + v) ^ (r & 7);
+        for (int v = 0; v < 4; ++v) {
+          const int chunk = (c * 4 + v) ^ (r & 7);
           reinterpret_cast<float4*>(stage + r * HD)[chunk] =
               make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
                           __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
         }
       }
       if (qrow < rows) {
-        const size_t at = static_cast<size_t>(s.t0 + tok_r) * p.Hq + h_r;
-        if (p.n_splits == 1) {
-          if (p.lse) p.lse[at] = lse_nat;
-        } else {
-          p.part_lse[static_cast<size_t>(split) * bt.T * p.Hq + at] = lse_nat;
-        }
+        const int tok = token_of(p, qrow);
+        const size_t at =
+            static_cast<size_t>(s.t0 + tok) * p.Hq + g * p.group + qrow - tok * p.group;
+        const float z = l == 0.f ? -INFINITY : (m - P_SHIFT + log2f(l)) * 0.69314718055994531f;
+        if (p.n_splits > 1)
+          p.part_lse[static_cast<size_t>(split) * bt.T * p.Hq + at] = z;
+        else if (p.lse)
+          p.lse[at] = z;
       }
-    }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + X), "r"(BQ) : "memory");
-    if (fin) {
+      __syncwarp();  // a warp writes the rows that it staged
       constexpr int CPR = HD / 4;
-      constexpr int RPW = 32 / CPR == 0 ? 1 : 32 / CPR;  // rows per warp and pass
+      constexpr int RPW = 32 / CPR;  // rows per pass (1 or 2)
       const int cc = lane % CPR;
-      for (int rr = quarter * RPW + lane / CPR; rr < BQ; rr += 4 * RPW) {
+#pragma unroll 4
+      for (int k = 0; k < 32; k += RPW) {
+        const int rr = quarter * 32 + k + lane / CPR;
         const int pr = first + X * BQ + rr;
-        if (pr >= rows) break;
-        const int tok = pr / p.group;
-        const int h = g * p.group + pr - tok * p.group;
-        const float4 v = reinterpret_cast<const float4*>(stage + rr * HD)[cc ^ (rr & 7)];
-        if (p.n_splits == 1) {
-          *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(s.t0 + tok) * p.ldo +
-                                    static_cast<size_t>(h) * HD + cc * 4) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        } else {
-          const size_t row = (static_cast<size_t>(split) * bt.T + s.t0 + tok) * p.Hq + h;
-          reinterpret_cast<float4*>(p.part_o + row * HD)[cc] = v;
+        if (pr < rows) {
+          const int tok = token_of(p, pr);
+          const int h = g * p.group + pr - tok * p.group;
+          const float4 v = reinterpret_cast<const float4*>(stage + rr * HD)[cc ^ (rr & 7)];
+          if (p.n_splits == 1) {
+            *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(s.t0 + tok) * p.ldo +
+                                      static_cast<size_t>(h) * HD + cc * 4) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          } else {
+            const size_t row = (static_cast<size_t>(split) * bt.T + s.t0 + tok) * p.Hq + h;
+            reinterpret_cast<float4*>(p.part_o + row * HD)[cc] = v;
+          }
         }
       }
     }
@@ -756,7 +795,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
   if (threadIdx.x >= 64 && threadIdx.x < 64 + NR) {
     const int r = static_cast<int>(threadIdx.x) - 64;
     sM[r] = -INFINITY;
-    sSees[r] = p.causal ? min(total, s.c0 + r / p.group + 1) : total;
+    sSees[r] = p.causal ? min(total, s.c0 + token_of(p, r) + 1) : total;
   }
   tc_fence_before();
   __syncthreads();
@@ -848,7 +887,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
     const int quarter = warp & 3;
     const int kl = quarter * 32 + lane;  // key of the tile; later element of the head
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    load_q_rows<HD>(p, s, g, 0, rows, sQ, sQ + NR * HD, sF, (warp - 2) * (NR / 4), NR / 4);
+    load_q_rows<HD, NR / 4>(p, s, g, 0, rows, sQ, sQ + NR * HD, sF, (warp - 2) * (NR / 4));
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
@@ -1038,7 +1077,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
     const size_t part = static_cast<size_t>(split) * bt.T * p.Hq;
     if (ok && kl < rows) {
       const float sum = (sRed[kl] + sRed[NR + kl]) + (sRed[2 * NR + kl] + sRed[3 * NR + kl]);
-      const int tok = kl / p.group;
+      const int tok = token_of(p, kl);
       const size_t at = static_cast<size_t>(s.t0 + tok) * p.Hq + g * p.group + kl - tok * p.group;
       const float z = sum == 0.f ? -INFINITY
                                  : (sM[kl] - N_SHIFT + log2f(sum)) * 0.69314718055994531f;
