@@ -31,6 +31,17 @@ constexpr int BQ = 128;
 constexpr int BKV = 128;
 constexpr int MAX_TILES = 128;  // key tiles per CTA: their page ids and scales sit in shared memory
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Order this thread's shared-memory writes before later accesses of the async
 // proxy (the tensor core's operand reads).
 __device__ __forceinline__ void fence_async_smem() {
@@ -190,10 +201,10 @@ __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, i
 // Many query rows per kv head: two 128-row query tiles per CTA
 // ---------------------------------------------------------------------------
 // Four warpgroups, with registers moved to the softmax (setmaxnreg):
-//   warps 0..3    0 = TMA producer, 1 = TMEM owner + MMA issuer (40 registers)
+//   warps 0..3    0 = TMA producer, 1 = TMEM owner + MMA issuer (80 registers)
 //   warps 4..11   softmax of tile A / B, one query row per thread (192)
 //   warps 12..15  V expansion: codes -> f16 tiles in shared memory, rows past
-//                 the visible keys zeroed (88)
+//                 the visible keys zeroed (48)
 // A softmax thread holds its 128 scores in registers between the maximum and
 // the exponentials, and hands P over in two halves of 64 keys, so that P V
 // starts while the second half is still being formed.
@@ -213,7 +224,7 @@ struct Wide {
   static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(BQ, HD);
   static_assert(RING >= 2 * BQ * HD * 4, "O staging does not fit the rings");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(40 + 2 * 192 + 88 == 512, "register shares exceed the launch's 128 a thread");
+  static_assert(80 + 2 * 192 + 48 == 512, "register shares exceed the launch's 128 a thread");
 };
 
 template <int HD>
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   const uint32_t tmem = *tmem_holder;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       // Lane l loads page l of the tile.  A page outside the pool is reported
@@ -353,70 +364,86 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         for (int j = max(0, issued - CF::VST); j < issued; ++j)
           mbar_wait(&v8_full[j % CF::VST], (j / CF::VST) & 1, nullptr, 0x524);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      bool ok = mbar_wait(q_full, 0, abort_flag, 0x531);
-      const uint32_t q_base = smem_u32(sQ);
-      auto issue_s = [&](int X, int j) {  // S_X = (hi + lo) K^T
-        const uint32_t k_base = smem_u32(sK + (j % CF::KST) * CF::T_BYTES);
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < HD / 32; ++kk)
-            umma_ss_f8(tmem + X * 128,
-                       sdesc_rows<HD>(q_base + (2 * X + part) * CF::T_BYTES + kk * 32),
-                       sdesc_rows<HD>(k_base + kk * 32), CF::IDESC_S, (part | kk) ? 1u : 0u);
-        umma_commit(&s_full[X]);
+      // The whole warp walks the schedule, so that descriptors stay in uniform
+      // registers; an elected lane issues.
+      auto wait_all = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, site));
       };
-      auto issue_pv = [&](int X, int j) -> bool {
-        const uint32_t v_base = smem_u32(sV16 + (j % CF::HST) * CF::V16_BYTES);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait(&p_full[2 * X + half], j & 1, abort_flag, 0x533)) return false;
-          tc_fence_after();
+      bool ok = wait_all(q_full, 0, 0x531);
+      // Descriptors advance by adding to their address field (16-byte units).
+      const uint64_t q_desc = sdesc_rows<HD>(smem_u32(sQ));
+      const uint64_t k_desc = sdesc_rows<HD>(smem_u32(sK));
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV16), BKV * 128, 1024);
+      constexpr int TD = CF::T_BYTES >> 4;
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+      };
+      auto issue_s = [&](int X, int ks) {  // S_X = (hi + lo) K^T
+        const uint64_t kd = k_desc + ks * TD, qd = q_desc + 2 * X * TD;
+        if (elect_one()) {
 #pragma unroll
-          for (int k4 = 0; k4 < BKV / 32; ++k4) {
-            const int kk = half * (BKV / 32) + k4;
-            umma_ts(tmem + 256 + X * 128, tmem + X * 128 + kk * 8,
-                    sdesc_sw128(v_base + kk * 16 * 128, BKV * 128, 1024), CF::IDESC_PV,
-                    (j | kk) ? 1u : 0u);
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < HD / 32; ++kk)
+              umma_ss_f8(tmem + X * 128, qd + (part * TD + kk * 2), kd + kk * 2, CF::IDESC_S,
+                         (part | kk) ? 1u : 0u);
+          umma_commit(&s_full[X]);
+        }
+      };
+      auto issue_pv = [&](int X, int j, int hs) -> bool {
+        const uint64_t vd = v_desc + hs * (CF::V16_BYTES >> 4);
+        const uint32_t d = tmem + 256 + X * 128, a = tmem + X * 128;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!wait_all(&p_full[2 * X + half], j & 1, 0x533)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = half * (BKV / 32); kk < (half + 1) * (BKV / 32); ++kk)
+              umma_ts(d, a + kk * 8, vd + kk * (16 * 128 / 16), CF::IDESC_PV,
+                      kk ? 1u : (j ? 1u : 0u));
           }
         }
         return true;
       };
-      if (ok) ok = mbar_wait(&k_full[0], 0, abort_flag, 0x532);
+      if (ok) ok = wait_all(&k_full[0], 0, 0x532);
       if (ok) {
         tc_fence_after();
         issue_s(0, 0);
         if (vB) issue_s(1, 0);
-        umma_commit(&k_empty[0]);
+        commit(&k_empty[0]);
       }
+      int ks = 0, kph = 0, hs = 0, hph = 0;  // stages and phases of K and of V f16
       for (int j = 0; ok && j < n; ++j) {
-        ok = mbar_wait(&v16_full[j % CF::HST], (j / CF::HST) & 1, abort_flag, 0x534);
-        if (ok) ok = issue_pv(0, j);
-        const bool more = j + 1 < n;
-        const int ks = (j + 1) % CF::KST;
-        if (ok && more) {
-          ok = mbar_wait(&k_full[ks], ((j + 1) / CF::KST) & 1, abort_flag, 0x532);
-          if (ok) {
-            tc_fence_after();
-            issue_s(0, j + 1);
-          }
+        if (++ks == CF::KST) {
+          ks = 0;
+          kph ^= 1;
         }
-        if (ok && vB) ok = issue_pv(1, j);
-        if (ok) umma_commit(&v16_empty[j % CF::HST]);
+        const bool more = j + 1 < n;
+        ok = wait_all(&v16_full[hs], hph, 0x534);
+        if (ok && more) ok = wait_all(&k_full[ks], kph, 0x532);
+        if (ok) ok = issue_pv(0, j, hs);
+        if (ok && more) issue_s(0, ks);
+        if (ok && vB) ok = issue_pv(1, j, hs);
+        if (ok) commit(&v16_empty[hs]);
         if (ok && more) {
-          if (vB) issue_s(1, j + 1);
-          umma_commit(&k_empty[ks]);
+          if (vB) issue_s(1, ks);
+          commit(&k_empty[ks]);
+        }
+        if (++hs == CF::HST) {
+          hs = 0;
+          hph ^= 1;
         }
       }
-      if (ok) umma_commit(o_final);
-      umma_commit(drain);
+      if (ok) commit(o_final);
+      commit(drain);
       mbar_wait(drain, 0, nullptr, 0x535);
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ V expansion
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     const int tid = static_cast<int>(threadIdx.x) - 384;
     // scales of the whole key range, and the largest V scale among them
     int emax = 0;
@@ -540,21 +567,47 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         for (int c = 0; c < 128; ++c)
           if (c > lim) sa[c] = __float_as_uint(-INFINITY);
       }
-      float tmax = -INFINITY;
+      // 32 keys from column c0: P as packed f16 pairs, their sum added to rs
+      float rs[4] = {0.f, 0.f, 0.f, 0.f};
+      auto probs = [&](const uint32_t* x, float f0, float f1, float neg_m, uint32_t* pk) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float m0 = __uint_as_float(sa[16 * q]), m1 = __uint_as_float(sa[16 * q + 1]);
-#pragma unroll
-        for (int c = 2; c < 16; c += 2) {
-          m0 = fmaxf(m0, __uint_as_float(sa[16 * q + c]));
-          m1 = fmaxf(m1, __uint_as_float(sa[16 * q + c + 1]));
+        for (int c = 0; c < 16; ++c) {
+          const float f = c < 8 ? f0 : f1;
+          const float p0 = attn::fast_exp2(fmaf(__uint_as_float(x[2 * c]), f, neg_m));
+          const float p1 = attn::fast_exp2(fmaf(__uint_as_float(x[2 * c + 1]), f, neg_m));
+          rs[(2 * c) & 3] += p0;
+          rs[(2 * c + 1) & 3] += p1;
+          const __half2 a = __floats2half2_rn(p0, p1);
+          pk[c] = *reinterpret_cast<const uint32_t*>(&a);
         }
-        tmax = fmaxf(tmax, fmaxf(m0, m1) * scg[q]);
+      };
+      // The first 64 keys' exponentials are formed with the maximum as it
+      // stands while the tile's own maximum is found beside them (the special
+      // function unit is what bounds this loop; the maximum is free there).
+      // Only where it grew by more than 2^8 are they formed again.
+      uint32_t pk[32];
+      float tmax = -INFINITY;
+      {
+        const float neg_m = P_SHIFT - m;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          probs(&sa[32 * h], scg[2 * h], scg[2 * h + 1], neg_m, &pk[16 * h]);
+#pragma unroll
+          for (int q = 4 * h; q < 4 * h + 4; ++q) {
+            float m0 = __uint_as_float(sa[16 * q]), m1 = __uint_as_float(sa[16 * q + 1]);
+#pragma unroll
+            for (int c = 2; c < 16; c += 2) {
+              m0 = fmaxf(m0, __uint_as_float(sa[16 * q + c]));
+              m1 = fmaxf(m1, __uint_as_float(sa[16 * q + c + 1]));
+            }
+            tmax = fmaxf(tmax, fmaxf(m0, m1) * scg[q]);
+          }
+        }
       }
-      // Raise the running max only when it grows by more than 2^8 (1/l keeps
-      // this exact).  PV_X(j-1) is complete because S_X(j) is.
       const bool want = tmax > m + attn::kRescaleThreshold || m == -INFINITY;
       if (__any_sync(0xffffffffu, want)) {
+        // Raise the maximum (1/l keeps a lagging one exact).  PV_X(j-1) is
+        // complete because S_X(j) is.
         const float m_new = fmaxf(tmax, m);
         if (j > 0) {
           const float f = (m == -INFINITY) ? 0.f : attn::fast_exp2(m - m_new);
@@ -570,29 +623,23 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           l *= f;
         }
         m = m_new;
+        const float neg_m = (m == -INFINITY) ? 0.f : P_SHIFT - m;
+        rs[0] = rs[1] = rs[2] = rs[3] = 0.f;
+        probs(&sa[0], scg[0], scg[1], neg_m, &pk[0]);
+        probs(&sa[32], scg[2], scg[3], neg_m, &pk[16]);
       }
+      // P takes the first half of S's columns
+      tmem_st32(tS, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[2 * X]);
       const float neg_m = (m == -INFINITY) ? 0.f : P_SHIFT - m;
-      float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float f = scg[2 * h + (c >> 3)];
-          const float p0 = attn::fast_exp2(fmaf(__uint_as_float(sa[32 * h + 2 * c]), f, neg_m));
-          const float p1 = attn::fast_exp2(fmaf(__uint_as_float(sa[32 * h + 2 * c + 1]), f, neg_m));
-          rs[(2 * c) & 3] += p0;
-          rs[(2 * c + 1) & 3] += p1;
-          const __half2 a = __floats2half2_rn(p0, p1);
-          pk[c] = *reinterpret_cast<const uint32_t*>(&a);
-        }
-        tmem_st16(tS + h * 16, pk);  // P takes the first half of S's columns
-        if (h & 1) {
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_full[2 * X + (h >> 1)]);
-        }
-      }
+      probs(&sa[64], scg[4], scg[5], neg_m, &pk[0]);
+      probs(&sa[96], scg[6], scg[7], neg_m, &pk[16]);
+      tmem_st32(tS + 32, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[2 * X + 1]);
       l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
     }
     const bool fin = __all_sync(0xffffffffu, ok && mbar_wait(o_final, 0, abort_flag, 0x553));
@@ -843,16 +890,22 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       bool ok = mbar_wait(q_full, 0, abort_flag, 0x571);
-      const uint32_t q_base = smem_u32(sQ), p_base = smem_u32(sP);
+      const uint64_t q_desc = sdesc_rows<HD>(smem_u32(sQ));
+      const uint64_t k_desc = sdesc_rows<HD>(smem_u32(sK));
+      // 32 keys a step: four 8-row groups of V and of P
+      const uint64_t v_desc = HD == 128 ? sdesc_sw128(smem_u32(sV), 1024, 1024)
+                                        : sdesc_sw64(smem_u32(sV), 512, 512);
+      const uint64_t p_desc = NR == 16 ? sdesc_sw64(smem_u32(sP), 512, 512)
+                                       : sdesc_sw128(smem_u32(sP), 1024, 1024);
       auto issue_s = [&](int j) -> bool {
         const int st = j % ST;
         if (!mbar_wait(&k_full[st], (j / ST) & 1, abort_flag, 0x572)) return false;
         tc_fence_after();
-        const uint32_t k_base = smem_u32(sK + st * CF::T_BYTES);
+        const uint64_t kd = k_desc + st * (CF::T_BYTES >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 32; ++kk)
-          umma_ss_f8(tmem + (j & 1) * 2 * NR, sdesc_rows<HD>(k_base + kk * 32),
-                     sdesc_rows<HD>(q_base + kk * 32), CF::IDESC_S, kk ? 1u : 0u);
+          umma_ss_f8(tmem + (j & 1) * 2 * NR, kd + kk * 2, q_desc + kk * 2, CF::IDESC_S,
+                     kk ? 1u : 0u);
         umma_commit(&s_full[j & 1]);
         umma_commit(&k_empty[st]);
         return true;
@@ -865,16 +918,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
         if (ok) ok = mbar_wait(p_full, j & 1, abort_flag, 0x574);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t v_base = smem_u32(sV + st * CF::T_BYTES);
+        const uint64_t vd = v_desc + st * (CF::T_BYTES >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BKV / 32; ++kk) {
-          // 32 keys: four 8-row groups of V and of P
-          const uint64_t da = HD == 128 ? sdesc_sw128(v_base + kk * 32 * 128, 1024, 1024)
-                                        : sdesc_sw64(v_base + kk * 32 * 64, 512, 512);
-          const uint64_t db = NR == 16 ? sdesc_sw64(p_base + kk * 32 * 64, 512, 512)
-                                       : sdesc_sw128(p_base + kk * 32 * 128, 1024, 1024);
-          umma_ss_f8(tmem + 4 * NR, da, db, CF::IDESC_PV, (j | kk) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < BKV / 32; ++kk)
+          umma_ss_f8(tmem + 4 * NR, vd + kk * (32 * HD / 16), p_desc + kk * (32 * CF::PB / 16),
+                     CF::IDESC_PV, kk ? 1u : (j ? 1u : 0u));
         umma_commit(pv_done);
         umma_commit(&v_empty[st]);
         if (j + 2 < n) ok = issue_s(j + 2);
