@@ -1766,9 +1766,9 @@ int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uin
   dg::paged::AttnParams p;
   p.bt = {B, T, max_new, max_pages, page, log2_of(page), n_pages, tok_start, cache_len, page_table};
   p.Hq = Hq; p.Hkv = Hkv; p.group = Hq / Hkv;
-  p.group_shift = 0;
-  while ((1ll << p.group_shift) < p.group) ++p.group_shift;
-  p.group_mul = p.group == 1 ? 0u : (uint32_t)((1ull << (31 + p.group_shift)) / p.group + 1);
+  p.group_shift = 31;
+  while ((1ll << (p.group_shift - 31)) < p.group) ++p.group_shift;
+  p.group_mul = (uint32_t)((1ull << p.group_shift) / p.group + 1);
   p.causal = mask_mode == DG_MASK_CAUSAL ? 1 : 0;
   p.max_prefix = max_prefix;
   p.n_pairs = pl.n_pairs;

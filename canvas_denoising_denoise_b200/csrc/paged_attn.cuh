@@ -100,13 +100,18 @@ struct AttnParams {
   float* part_lse;  // [n_splits, T, Hq]
 };
 
-// Token of a packed row below 2^31: row / group by a multiplication.  With s =
-// ceil(log2 group) and mul = floor(2^(31 + s) / group) + 1 < 2^32 the error
-// row (mul - 2^(31 + s) / group) / 2^(31 + s) stays below 1 / group.
+// Token of a packed row below 2^31: row / group by a multiplication.  With c =
+// ceil(log2 group), mul = floor(2^(31 + c) / group) + 1 and shift = 31 + c the
+// error row (mul - 2^shift / group) / 2^shift stays below 1 / group.
 __device__ __forceinline__ int token_of(const AttnParams& p, int row) {
-  return p.group == 1 ? row
-                      : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_mul) >>
-                                         (p.group_shift - 1));
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(row)) * p.group_mul) >>
+                          p.group_shift);
+}
+
+// The smallest e with amax <= 448 2^e = 1.75 2^(e + 8), at least -100, from
+// the bf16 bits of a finite amax.
+__device__ __forceinline__ int q_exponent(uint32_t top) {
+  return max(static_cast<int>(top >> 7) - 135 + ((top & 0x7Fu) > 0x60u ? 1 : 0), -100);
 }
 
 // Eight scaled query elements as e4m3 hi + lo.  x f (f a power of two) fits f16
@@ -182,8 +187,7 @@ __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, i
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = max(top & 0xFFFFu, top >> 16);
     const bool fine = top < 0x7F80u;
-    // the smallest e with amax <= 448 2^e = 1.75 2^(e + 8), at least -100
-    const int e = max(static_cast<int>(top >> 7) - 135 + ((top & 0x7Fu) > 0x60u ? 1 : 0), -100);
+    const int e = q_exponent(top);
     uint2 vh = make_uint2(0u, 0u), vl = make_uint2(0u, 0u);
     if (fine) split_q(x, pow2(-e), &vh, &vl);
     __syncwarp();  // the row has been read
@@ -193,6 +197,71 @@ __device__ __forceinline__ void load_q_rows(const AttnParams& p, const Seq& s, i
       *reinterpret_cast<uint2*>(hi + at) = vh;
       *reinterpret_cast<uint2*>(lo + at) = vl;
       if (c8 == 0) factor[r] = fine ? p.scale_log2 * pow2(e) : __int_as_float(0x7FC00000);
+    }
+  }
+}
+
+// The same for a 128-row tile by its four softmax warps, a thread per row: a row
+// is too long a chain of shuffles and conversions to walk 32 of them per warp
+// (7 us a CTA).  The bf16 rows land in `raw` (rows of 2 HD bytes, 16-byte chunk
+// c at c ^ (r & 7)): shared memory of ring stages that are not yet in use.
+template <int HD>
+__device__ __forceinline__ void load_q_tile(const AttnParams& p, const Seq& s, int g, int first,
+                                            int rows, uint8_t* raw, uint8_t* hi, uint8_t* lo,
+                                            float* factor, int r0, int row) {
+  constexpr int LANES = HD / 8;  // 16-byte chunks per row
+  constexpr int PER = 32 / LANES;
+  const int lane = lane_id();
+  const int c8 = lane % LANES;
+  const __nv_bfloat16* base = p.q + static_cast<size_t>(s.t0) * p.ldq +
+                              static_cast<size_t>(g) * p.group * HD + c8 * 8;
+  // each step's loads come before its stores: the compiler keeps their order,
+  // and a chain of one row's latency after another's is what this costs
+  constexpr int BATCH = 8;
+#pragma unroll 1
+  for (int u = 0; u < 32 / PER; u += BATCH) {
+    const __nv_bfloat16* src[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int pr = min(first + r0 + (u + i) * PER + lane / LANES, rows - 1);
+      const int tok = token_of(p, pr);
+      src[i] = base + static_cast<int64_t>(tok) * p.ldq + (pr - tok * p.group) * HD;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int r = r0 + (u + i) * PER + lane / LANES;
+      copy16_async(raw + r * (2 * HD) + ((c8 ^ (r & 7)) << 4), src[i], first + r < rows);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const uint8_t* mine = raw + row * (2 * HD);
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < LANES; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(mine + ((c ^ (row & 7)) << 4));
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                 __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  const bool fine = top < 0x7F80u;
+  const int e = fine ? q_exponent(top) : 0;
+  factor[row] = fine ? p.scale_log2 * pow2(e) : __int_as_float(0x7FC00000);
+  const float f = fine ? pow2(-e) : 0.f;  // a bad row's codes do not matter
+#pragma unroll 1
+  for (int c0 = 0; c0 < LANES; c0 += 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = *reinterpret_cast<const uint4*>(mine + (((c0 + i) ^ (row & 7)) << 4));
+    uint2 h[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_q(x[i], f, &h[i], &l[i]);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const int at = swz<HD>(row, (c0 + i) >> 1);
+      *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[i].x, h[i].y, h[i + 1].x, h[i + 1].y);
+      *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[i].x, l[i].y, l[i + 1].x, l[i + 1].y);
     }
   }
 }
@@ -223,6 +292,8 @@ struct Wide {
   static constexpr uint32_t IDESC_S = idesc_e4m3_f32(BQ, BKV);
   static constexpr uint32_t IDESC_PV = idesc_f16_f32_bmn(BQ, HD);
   static_assert(RING >= 2 * BQ * HD * 4, "O staging does not fit the rings");
+  static_assert(V16_BYTES == BQ * HD * 2 && (KST - 1) * T_BYTES >= BQ * HD * 2 && HST == 2,
+                "raw query rows do not fit the stages that they pass through");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(80 + 2 * 192 + 48 == 512, "register shares exceed the launch's 128 a thread");
 };
@@ -261,6 +332,31 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
   const int warp = warp_id();
   const int lane = lane_id();
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 8);
+    mbar_init(meta_full, 4);
+    for (int i = 0; i < CF::KST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < CF::VST; ++i) {
+      mbar_init(&v8_full[i], 1);
+      mbar_init(&v8_empty[i], 4);
+    }
+    for (int i = 0; i < CF::HST; ++i) {
+      mbar_init(&v16_full[i], 4);
+      mbar_init(&v16_empty[i], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], BQ);
+    mbar_init(o_final, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   griddep_wait();
   const Batch& bt = p.bt;
   // Causal launches take their heaviest row blocks (the last) first, so that
@@ -291,29 +387,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   const int n_pages = ((min(visible, (t_beg + n) * BKV) + bt.page - 1) >> bt.log_page) - page_beg;
   const int32_t* table = bt.page_table + static_cast<size_t>(b) * bt.max_pages + page_beg;
 
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, vB ? 8 : 4);
-    mbar_init(meta_full, 4);
-    for (int i = 0; i < CF::KST; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < CF::VST; ++i) {
-      mbar_init(&v8_full[i], 1);
-      mbar_init(&v8_empty[i], 4);
-    }
-    for (int i = 0; i < CF::HST; ++i) {
-      mbar_init(&v16_full[i], 4);
-      mbar_init(&v16_empty[i], 1);
-    }
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], BQ);
-    mbar_init(o_final, 1);
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -340,8 +413,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const int pg = next;
         if (lane < ppt && ((j + 1) << log_ppt) + lane < n_pages)
           next = table[((j + 1) << log_ppt) + lane];
-        bool ok =
-            j < CF::KST || mbar_wait(&k_empty[ks], ((j / CF::KST) - 1) & 1, abort_flag, 0x521);
+        bool ok = j == 1 ? mbar_wait(q_full, 0, abort_flag, 0x525)
+                         : j < CF::KST ||
+                               mbar_wait(&k_empty[ks], ((j / CF::KST) - 1) & 1, abort_flag, 0x521);
         ok = ok && (j < CF::VST ||
                     mbar_wait(&v8_empty[vs], ((j / CF::VST) - 1) & 1, abort_flag, 0x522));
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -482,8 +556,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     for (int j = 0; j < n; ++j) {
       const int vs = j % CF::VST, hs = j % CF::HST;
       bool ok = mbar_wait(&v8_full[vs], (j / CF::VST) & 1, abort_flag, 0x541);
-      ok = ok && (j < CF::HST ||
-                  mbar_wait(&v16_empty[hs], ((j / CF::HST) - 1) & 1, abort_flag, 0x542));
+      ok = ok && (j == 0 || (j == 1 ? mbar_wait(q_full, 0, abort_flag, 0x543)
+                                    : mbar_wait(&v16_empty[hs], ((j / CF::HST) - 1) & 1,
+                                                abort_flag, 0x542)));
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* src = sV8 + vs * CF::T_BYTES;
       uint8_t* dst = sV16 + hs * CF::V16_BYTES + half_off;
@@ -531,12 +606,16 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const int r = quarter * 32 + lane;
     const int qrow = first + X * BQ + r;  // packed row
     bool ok = X == 0 || vB;
+    // The raw rows pass through V f16's second stage (tile A) and the K codes'
+    // second and third (tile B); their first writers wait for q_full.
+    if (ok)
+      load_q_tile<HD>(p, s, g, first + X * BQ, rows,
+                      X == 0 ? sV16 + CF::V16_BYTES : sK + CF::T_BYTES, sQ + 2 * X * CF::T_BYTES,
+                      sQ + (2 * X + 1) * CF::T_BYTES, sQf + X * BQ, quarter * 32, r);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
     if (ok) {
-      load_q_rows<HD, 32>(p, s, g, first + X * BQ, rows, sQ + 2 * X * CF::T_BYTES,
-                          sQ + (2 * X + 1) * CF::T_BYTES, sQf + X * BQ, quarter * 32);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
       ok = __all_sync(0xffffffffu, mbar_wait(meta_full, 0, abort_flag, 0x552));
     }
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -654,16 +733,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(emax - 127 - V_SHIFT)) / l;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < HD / 16; ++c) {
-        uint32_t o[16];
-        tmem_ld16(tO + c * 16, o);
+      for (int c = 0; c < HD / 64; ++c) {
+        uint32_t o[2][32];
+        tmem_ld32(tO + c * 64, o[0]);
+        tmem_ld32(tO + c * 64 + 32, o[1]);
         tmem_ld_wait();
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int chunk = (c * 4 + v) ^ (r & 7);
-          reinterpret_cast<float4*>(stage + r * HD)[chunk] =
-              make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                          __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+        for (int v = 0; v < 16; ++v) {
+          const uint32_t* x = &o[v >> 3][(v & 7) * 4];
+          reinterpret_cast<float4*>(stage + r * HD)[(c * 16 + v) ^ (r & 7)] =
+              make_float4(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv,
+                          __uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
         }
       }
       if (qrow < rows) {
@@ -680,21 +760,30 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       constexpr int CPR = HD / 4;
       constexpr int RPW = 32 / CPR;  // rows per pass (1 or 2)
       const int cc = lane % CPR;
-#pragma unroll 4
-      for (int k = 0; k < 32; k += RPW) {
-        const int rr = quarter * 32 + k + lane / CPR;
-        const int pr = first + X * BQ + rr;
-        if (pr < rows) {
+      constexpr int BATCH = 8;  // loads ahead of the stores, as above
+#pragma unroll 1
+      for (int k0 = 0; k0 < 32; k0 += BATCH * RPW) {
+        float4 v[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int rr = quarter * 32 + k0 + i * RPW + lane / CPR;
+          v[i] = reinterpret_cast<const float4*>(stage + rr * HD)[cc ^ (rr & 7)];
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int pr = first + X * BQ + quarter * 32 + k0 + i * RPW + lane / CPR;
           const int tok = token_of(p, pr);
           const int h = g * p.group + pr - tok * p.group;
-          const float4 v = reinterpret_cast<const float4*>(stage + rr * HD)[cc ^ (rr & 7)];
-          if (p.n_splits == 1) {
-            *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(s.t0 + tok) * p.ldo +
-                                      static_cast<size_t>(h) * HD + cc * 4) =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-          } else {
-            const size_t row = (static_cast<size_t>(split) * bt.T + s.t0 + tok) * p.Hq + h;
-            reinterpret_cast<float4*>(p.part_o + row * HD)[cc] = v;
+          if (pr < rows) {
+            if (p.n_splits == 1) {
+              *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD +
+                                        cc * 4) =
+                  make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
+            } else {
+              const int64_t row =
+                  (static_cast<int64_t>(split) * bt.T + s.t0 + tok) * p.Hq + h;
+              reinterpret_cast<float4*>(p.part_o + row * HD)[cc] = v[i];
+            }
           }
         }
       }
@@ -802,6 +891,24 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
 
   const int warp = warp_id();
   const int lane = lane_id();
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, 128);
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   griddep_wait();
   const Batch& bt = p.bt;
   const int g = static_cast<int>(blockIdx.x) % p.Hkv;
@@ -819,22 +926,6 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
   const int pages = (total + bt.page - 1) >> bt.log_page;  // of the sequence
   const int32_t* table = bt.page_table + static_cast<size_t>(b) * bt.max_pages;
 
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, 4);
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(p_full, 128);
-    mbar_init(pv_done, 1);
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
   if (warp == 1) {
     tmem_alloc(tmem_holder, CF::TMEM);
     tmem_relinquish();
@@ -1178,6 +1269,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
 // w_s = 2^(lse_s - max).  A warp per (token, head); only the splits that the
 // row's visible keys reach were written, and only those are read, in order.
 // ---------------------------------------------------------------------------
+// Lane s reads split s's log-sum-exp, so every weight is known after one load;
+// the partial rows then come COMBINE_BATCH at a time, none waiting for another.
 constexpr int COMBINE_THREADS = 256;
 constexpr int COMBINE_BATCH = 8;
 
@@ -1200,37 +1293,42 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnPara
   float mx = -INFINITY, wsum = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int s0 = 0; s0 < S; s0 += COMBINE_BATCH) {
-    float ls[COMBINE_BATCH], v[COMBINE_BATCH][PER];
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const float z = s0 + lane < S ? p.part_lse[(s0 + lane) * stride + row] : -INFINITY;
+    float top = z;
+    bool bad = z != z;
 #pragma unroll
-    for (int k = 0; k < COMBINE_BATCH; ++k) {
-      const int sp = s0 + k;
-      ls[k] = sp < S ? p.part_lse[sp * stride + row] : -INFINITY;
-      const float* src = p.part_o + (sp * stride + row) * HD + lane * PER;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, mx);
+    const float f = mx == -INFINITY ? 0.f : expf(mx - top);
+    // a split without a visible key weighs nothing; a NaN one makes the row NaN
+    const float w = z == -INFINITY ? 0.f : bad ? z : expf(z - top);
+    wsum = wsum * f + warp_sum(w);
 #pragma unroll
-      for (int e = 0; e < PER; e += 2) {
-        const float2 f = sp < S ? *reinterpret_cast<const float2*>(src + e) : make_float2(0.f, 0.f);
-        v[k][e] = f.x;
-        v[k][e + 1] = f.y;
+    for (int e = 0; e < PER; ++e) acc[e] *= f;
+    mx = top;
+    const int here = min(32, S - s0);
+    for (int k0 = 0; k0 < here; k0 += COMBINE_BATCH) {
+      float v[COMBINE_BATCH][PER];
+#pragma unroll
+      for (int k = 0; k < COMBINE_BATCH; ++k) {
+        const float* src = p.part_o + ((s0 + k0 + k) * stride + row) * HD + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) {
+          const float2 x = k0 + k < here ? *reinterpret_cast<const float2*>(src + e)
+                                         : make_float2(0.f, 0.f);
+          v[k][e] = x.x;
+          v[k][e + 1] = x.y;
+        }
       }
-    }
-    float top = mx;
 #pragma unroll
-    for (int k = 0; k < COMBINE_BATCH; ++k) top = fmaxf(top, ls[k]);
-    if (top > mx) {
-      const float f = mx == -INFINITY ? 0.f : expf(mx - top);
+      for (int k = 0; k < COMBINE_BATCH; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        if (k0 + k < here) {
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] *= f;
-      wsum *= f;
-      mx = top;
-    }
-#pragma unroll
-    for (int k = 0; k < COMBINE_BATCH; ++k) {
-      if (ls[k] == -INFINITY) continue;  // no visible key in the split
-      const float w = expf(ls[k] - mx);
-      wsum += w;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+          for (int e = 0; e < PER; ++e) acc[e] = wk == 0.f ? acc[e] : fmaf(wk, v[k][e], acc[e]);
+        }
+      }
     }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
