@@ -31,6 +31,20 @@ constexpr int BQ = 128;
 constexpr int BKV = 128;
 constexpr int MAX_TILES = 128;  // key tiles per CTA: their page ids and scales sit in shared memory
 
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+constexpr int MAX_CLUSTER = 8;  // portable cluster size
+
+// Largest value over a warp (NaN ignored).
+__device__ __forceinline__ float warp_top(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -89,6 +103,7 @@ struct AttnParams {
   int n_pairs;           // query-row blocks (of 256 packed rows) per kv head
   int tiles_per_split;   // key tiles per CTA
   int n_splits;
+  int merge;             // the splits of a unit form a cluster, which merges them
   float scale_log2;      // scale * log2(e)
   const __nv_bfloat16* q;
   int ldq;
@@ -96,7 +111,7 @@ struct AttnParams {
   __nv_bfloat16* out;
   int ldo;
   float* lse;       // [T, Hq] or null
-  float* part_o;    // [n_splits, T, Hq, hd] (n_splits > 1)
+  float* part_o;    // [n_splits, T, Hq, hd] (n_splits > 1 without merge)
   float* part_lse;  // [n_splits, T, Hq]
 };
 
@@ -921,12 +936,13 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
   const int tiles = (total + BKV - 1) / BKV;
   const int t_beg = split * p.tiles_per_split;
   const int n = min(tiles, t_beg + p.tiles_per_split) - t_beg;
-  if (n <= 0) return;
+  const bool idle = n <= 0;  // no key of this split exists
+  if (idle && !p.merge) return;
   const int log_ppt = 7 - bt.log_page;
   const int pages = (total + bt.page - 1) >> bt.log_page;  // of the sequence
   const int32_t* table = bt.page_table + static_cast<size_t>(b) * bt.max_pages;
 
-  if (warp == 1) {
+  if (warp == 1 && !idle) {
     tmem_alloc(tmem_holder, CF::TMEM);
     tmem_relinquish();
   }
@@ -941,7 +957,9 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
   griddep_launch();  // only now: a successor's CTA must not take the TMEM before this one
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == 0) {
+  if (idle) {
+    if (threadIdx.x < NR) sF[threadIdx.x] = 0.f;  // no weight; the maximum stays at -inf
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int ppt = 1 << log_ppt;
     const int page_bytes = bt.page * HD;
@@ -1113,9 +1131,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
         scores(ev, false);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float v = x[r];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          const float v = warp_top(x[r]);
           if (lane == 0) sRed[quarter * NR + r] = v;
         }
         if (j > 0) {
@@ -1207,17 +1223,40 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
     ok = __all_sync(0xffffffffu, ok && j == n &&
                                      mbar_wait(pv_done, (n - 1) & 1, abort_flag, 0x585));
     tc_fence_after();
+    // sum of l over the warp's 32 keys for all rows at once: each exchange
+    // halves the rows that a lane still carries
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float v = warp_sum(l[r]);
-      if (lane == 0) sRed[quarter * NR + r] = v;
+    for (int half = NR / 2, bit = 16; bit > 0; bit >>= 1, half >>= 1) {
+      const bool up = (lane & bit) != 0;
+      if (half > 0) {
+#pragma unroll
+        for (int r = 0; r < half; ++r) {
+          const float give = up ? l[r] : l[r + half];
+          const float keep = up ? l[r + half] : l[r];
+          l[r] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+        }
+      } else {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], bit);
+      }
+    }
+    // lane bits from the top select the row: bit 16 its highest bit, and so on
+    {
+      const int r = NR == 32 ? lane : lane >> 1;
+      if (NR == 32 || (lane & 1) == 0) sRed[quarter * NR + r] = l[0];
     }
     bar_any(1, 128, false);
-    const size_t part = static_cast<size_t>(split) * bt.T * p.Hq;
-    if (ok && kl < rows) {
-      const float sum = (sRed[kl] + sRed[NR + kl]) + (sRed[2 * NR + kl] + sRed[3 * NR + kl]);
+    // O^T, a thread per element of the head: value of row r in terms of 2^-m
+    float* sO = reinterpret_cast<float*>(sK);  // [NR][HD]; the K stages are idle now
+    const int64_t part = static_cast<int64_t>(split) * bt.T * p.Hq;
+    float sum = 0.f;
+    if (kl < NR) {
+      sum = (sRed[kl] + sRed[NR + kl]) + (sRed[2 * NR + kl] + sRed[3 * NR + kl]);
+      if (!ok) sum = 0.f;
+      sF[kl] = p.merge ? sum : (sum == 0.f ? 0.f : 1.f / sum);
+    }
+    if (kl < rows && !p.merge) {
       const int tok = token_of(p, kl);
-      const size_t at = static_cast<size_t>(s.t0 + tok) * p.Hq + g * p.group + kl - tok * p.group;
+      const int64_t at = static_cast<int64_t>(s.t0 + tok) * p.Hq + g * p.group + kl - tok * p.group;
       const float z = sum == 0.f ? -INFINITY
                                  : (sM[kl] - N_SHIFT + log2f(sum)) * 0.69314718055994531f;
       if (p.n_splits > 1)
@@ -1225,6 +1264,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
       else if (p.lse)
         p.lse[at] = z;
     }
+    bar_any(1, 128, false);
     int tok = 0, hh = 0;
 #pragma unroll
     for (int c = 0; c < NR; c += 16) {
@@ -1234,31 +1274,78 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
       tmem_ld16(tl + 5 * NR + c, o1);
       tmem_ld16(tl + 6 * NR + c, o2);
       tmem_ld_wait();
+      if (kl < HD) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = c + e;
-        if (r < rows && ok && kl < HD) {
-          const float sum = (sRed[r] + sRed[NR + r]) + (sRed[2 * NR + r] + sRed[3 * NR + r]);
+        for (int e = 0; e < 16; ++e) {
+          const int r = c + e;
+          if (r >= rows) break;
           const float v = fmaf(__uint_as_float(o2[e]), 1.f / 256.f,
-                               fmaf(__uint_as_float(o1[e]), 1.f / 16.f, __uint_as_float(o0[e]))) *
-                          (sum == 0.f ? 0.f : 1.f / sum);
+                               fmaf(__uint_as_float(o1[e]), 1.f / 16.f, __uint_as_float(o0[e])));
           const int h = g * p.group + hh;
-          if (p.n_splits > 1)
-            p.part_o[(part + static_cast<size_t>(s.t0 + tok) * p.Hq + h) * HD + kl] = v;
+          if (p.merge)
+            sO[r * HD + kl] = v;
+          else if (p.n_splits > 1)
+            p.part_o[(part + static_cast<int64_t>(s.t0 + tok) * p.Hq + h) * HD + kl] = v * sF[r];
           else
-            p.out[static_cast<size_t>(s.t0 + tok) * p.ldo + static_cast<size_t>(h) * HD + kl] =
-                __float2bfloat16_rn(v);
-        }
-        if (++hh == p.group) {
-          hh = 0;
-          ++tok;
+            p.out[static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD + kl] =
+                __float2bfloat16_rn(v * sF[r]);
+          if (++hh == p.group) {
+            hh = 0;
+            ++tok;
+          }
         }
       }
     }
   }
+  if (p.merge) {
+    // Every split's O, sums (sF) and maxima (sM) lie in its CTA's shared
+    // memory; the CTAs of the cluster share the rows x hd results.
+    cluster_arrive_wait();
+    if (threadIdx.x >= 64) {
+      const int S = p.n_splits;
+      uint32_t o_at[MAX_CLUSTER], f_at[MAX_CLUSTER], m_at[MAX_CLUSTER];
+#pragma unroll
+      for (int k = 0; k < MAX_CLUSTER; ++k) {
+        o_at[k] = cluster_addr(sK, min(k, S - 1));
+        f_at[k] = cluster_addr(sF, min(k, S - 1));
+        m_at[k] = cluster_addr(sM, min(k, S - 1));
+      }
+      for (int i = split * 128 + static_cast<int>(threadIdx.x) - 64; i < rows * HD; i += S * 128) {
+        const int r = i / HD;
+        float o[MAX_CLUSTER], f[MAX_CLUSTER], m[MAX_CLUSTER];
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k) {
+          m[k] = k < S ? ld_cluster(m_at[k] + r * 4) : -INFINITY;
+          f[k] = k < S ? ld_cluster(f_at[k] + r * 4) : 0.f;
+          o[k] = k < S ? ld_cluster(o_at[k] + i * 4) : 0.f;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k) top = fmaxf(top, m[k]);
+        float sum = 0.f, v = 0.f;
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k) {
+          // a split without a visible key left its O unwritten
+          if (f[k] != 0.f) {
+            const float e = m[k] == -INFINITY ? 1.f : attn::fast_exp2(m[k] - top);
+            sum = fmaf(e, f[k], sum);
+            v = fmaf(e, o[k], v);
+          }
+        }
+        const int tok = token_of(p, r);
+        const int h = g * p.group + r - tok * p.group;
+        p.out[static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD + (i & (HD - 1))] =
+            __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+        if (p.lse && (i & (HD - 1)) == 0)
+          p.lse[static_cast<int64_t>(s.t0 + tok) * p.Hq + h] =
+              sum == 0.f ? -INFINITY : (top - N_SHIFT + log2f(sum)) * 0.69314718055994531f;
+      }
+    }
+    cluster_arrive_wait();  // no CTA leaves while another reads its shared memory
+  }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 1 && !idle) {
     tc_fence_after();
     tmem_dealloc(tmem, CF::TMEM);
   }
