@@ -694,45 +694,65 @@ int launch_append(const dg::paged::AppendParams& p, int blocks, cudaStream_t s) 
 // Execution plan of the paged attention, from the shape's bounds alone (so a
 // shape always gives the same bits).  Up to 32 packed rows per kv head run with
 // keys along the tensor core's M (narrow_kernel, `rows` = 16 or 32), more with
-// 256-row query blocks (wide_kernel, rows = 0).  The key range is split so that
-// the SMs are filled once (wide; splits of two tiles at least), or a few times
-// over (narrow, two CTAs per SM: unequal lengths then even out).
+// 256-row query blocks (wide_kernel, rows = 0).
 struct PagedPlan {
   int rows, n_pairs, tiles_per_split, n_splits;
-  bool merge;  // the splits of a unit run as one cluster and merge in shared memory
+  bool merge;   // the splits of a unit run as one cluster and merge in shared memory
+  bool sorted;  // more CTAs than fit at once: the longest sequences first
 };
 
-PagedPlan plan_paged(int B, int Hq, int Hkv, int max_new, long long max_keys) {
+// The split of `tiles` key tiles that ends soonest when `units` x splits CTAs
+// run `slots` at a time: a CTA costs its tiles and `fixed` tiles' time, a merge
+// of the splits `merge` once.
+int best_splits(long long units, int tiles, int slots, int fixed, int merge, int most) {
+  int best = 1;
+  long long least = -1;
+  for (int s = 1; s <= std::min(tiles, most); ++s) {
+    const long long waves = (units * s + slots - 1) / slots;
+    const long long cost = waves * (cdiv(tiles, s) + fixed) + (s > 1 ? merge : 0);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+PagedPlan plan_paged(int B, int Hq, int Hkv, int hd, int max_new, long long max_keys, bool causal) {
   using namespace dg::paged;
   PagedPlan pl;
   pl.merge = false;
   const int rows = Hq / Hkv * max_new;
   const int tiles = (int)std::max(1ll, (max_keys + BKV - 1) / BKV);
-  int per;
+  int splits, slots;
+  long long units;
   if (rows <= 32) {
     pl.rows = rows <= 16 ? 16 : 32;
     pl.n_pairs = 1;
-    const long long units = (long long)B * Hkv;
-    const long long even = (units * tiles + 2 * kNumSMs - 1) / (2 * kNumSMs);
-    per = (int)std::min<long long>(std::max(1ll, even), 64);
+    units = (long long)B * Hkv;
+    slots = kNumSMs * (pl.rows == 32 ? 1 : hd == 128 ? 2 : 3);
+    splits = best_splits(units, tiles, slots, 4, 4, kNumSMs * 2);
     // Few units: as many splits as a cluster holds, merged by it (13.4 us, one
     // token over 4096 keys and 8 kv heads; 14.5 with a second launch), unless
     // they would be long or the clusters more than the GPU places at once.
-    const int merged = cdiv(tiles, MAX_CLUSTER);
-    pl.merge = tiles > 1 && units * MAX_CLUSTER <= kNumSMs && merged <= 8;
-    if (pl.merge) per = std::max(per, merged);
+    if (tiles > 1 && units * MAX_CLUSTER <= kNumSMs && cdiv(tiles, MAX_CLUSTER) <= 8) {
+      splits = std::min(splits, MAX_CLUSTER);
+      pl.merge = true;
+    }
   } else {
     pl.rows = 0;
     pl.n_pairs = cdiv(rows, 2 * BQ);
-    const long long units = (long long)B * Hkv * pl.n_pairs;
-    int s = (int)std::max(1ll, kNumSMs / units);
-    s = std::min(s, std::max(1, tiles / 2));
-    per = std::min(cdiv(tiles, s), MAX_TILES);
+    units = (long long)B * Hkv * pl.n_pairs;
+    slots = kNumSMs;
+    // a causal launch's row blocks see half the new keys on average, and its
+    // grid has the long ones first: with enough of them it needs no split
+    splits = causal && units >= slots ? 1 : best_splits(units, tiles, slots, 4, 4, kNumSMs);
+    splits = std::max(splits, cdiv(tiles, MAX_TILES));
   }
-  pl.n_splits = cdiv(tiles, per);
-  pl.tiles_per_split = cdiv(tiles, pl.n_splits);
+  pl.tiles_per_split = cdiv(tiles, splits);
   pl.n_splits = cdiv(tiles, pl.tiles_per_split);
   pl.merge = pl.merge && pl.n_splits > 1;
+  pl.sorted = B > 1 && B <= MAX_SORTED && units * pl.n_splits > slots;
   return pl;
 }
 
@@ -1738,8 +1758,10 @@ size_t dg_paged_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int hd, int 
       max_new <= 0 || max_prefix < 0 || (long long)(Hq / Hkv) * std::min(max_new, T) > (1 << 30))
     return 0;
   max_new = std::min(max_new, T);
-  return paged_ws_bytes(plan_paged(B, Hq, Hkv, max_new, (long long)max_prefix + max_new), T, Hq,
-                        hd);
+  const long long keys = (long long)max_prefix + max_new;
+  // whichever mask: the larger of the two plans' needs
+  return std::max(paged_ws_bytes(plan_paged(B, Hq, Hkv, hd, max_new, keys, false), T, Hq, hd),
+                  paged_ws_bytes(plan_paged(B, Hq, Hkv, hd, max_new, keys, true), T, Hq, hd));
 }
 
 int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uint8_t* v_pages,
@@ -1767,7 +1789,8 @@ int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uin
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: too many rows per kv head", fn);
   if (max_new == 0) return DG_OK;
   // planned from the bounds alone, as the workspace query is
-  const PagedPlan pl = plan_paged(B, Hq, Hkv, max_new, (long long)max_prefix + max_new);
+  const PagedPlan pl = plan_paged(B, Hq, Hkv, hd, max_new, (long long)max_prefix + max_new,
+                                  mask_mode == DG_MASK_CAUSAL);
   if ((long long)B * Hkv * pl.n_pairs > 0x7FFFFFFFll || pl.n_splits > 65535 ||
       (long long)max_new * Hq > 0x7FFFFF00ll)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: too many rows for one launch", fn);
@@ -1786,6 +1809,7 @@ int dg_paged_attn_e4m3(const void* q, int ldq, const uint8_t* k_pages, const uin
   p.tiles_per_split = pl.tiles_per_split;
   p.n_splits = pl.n_splits;
   p.merge = pl.merge ? 1 : 0;
+  p.sorted = pl.sorted ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.q = (const __nv_bfloat16*)q;
   p.ldq = ldq;

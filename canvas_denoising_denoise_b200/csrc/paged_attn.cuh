@@ -103,6 +103,7 @@ struct AttnParams {
   int n_pairs;           // query-row blocks (of 256 packed rows) per kv head
   int tiles_per_split;   // key tiles per CTA
   int n_splits;
+  int sorted;            // CTAs outnumber the slots: longest sequences first
   int merge;             // the splits of a unit form a cluster, which merges them
   float scale_log2;      // scale * log2(e)
   const __nv_bfloat16* q;
@@ -281,6 +282,31 @@ __device__ __forceinline__ void load_q_tile(const AttnParams& p, const Seq& s, i
   }
 }
 
+// The sequence that comes `want`-th by cached and new rows, longest first (ties
+// to the lower index): CTAs start in grid order, and with more of them than fit
+// at once the long ones must not be the last.  Every thread of the CTA calls it.
+constexpr int MAX_SORTED = 256;
+__device__ __forceinline__ int nth_longest(const Batch& bt, int want, int* scratch, int threads) {
+  int* len = scratch + 1;
+  for (int i = threadIdx.x; i < bt.B; i += threads) {
+    const int n = bt.tok_start[i + 1] - bt.tok_start[i];
+    len[i] = n > 0 ? bt.cache_len[i] + n : 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < bt.B; i += threads) {
+    const int mine = len[i];
+    int before = 0;
+#pragma unroll 8
+    for (int k = 0; k < bt.B; ++k) {
+      const int v = len[k];
+      before += (v > mine || (v == mine && k < i)) ? 1 : 0;
+    }
+    if (before == want) *scratch = i;
+  }
+  __syncthreads();
+  return *scratch;
+}
+
 // ---------------------------------------------------------------------------
 // Many query rows per kv head: two 128-row query tiles per CTA
 // ---------------------------------------------------------------------------
@@ -382,7 +408,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   const int gb = p.causal ? static_cast<int>(blockIdx.x) % nbg
                           : static_cast<int>(blockIdx.x) / p.n_pairs;
   const int g = gb % p.Hkv;
-  const int b = gb / p.Hkv;
+  const int b = p.sorted ? nth_longest(bt, gb / p.Hkv, reinterpret_cast<int*>(sQ), WIDE_THREADS)
+                         : gb / p.Hkv;
   const int split = blockIdx.y;
   const Seq s = load_seq(bt, b, p.max_prefix, 0x511,
                          threadIdx.x == 0 && split == 0 && pi == 0 && g == 0);
@@ -875,7 +902,7 @@ __device__ __forceinline__ int p_swz(int r, int c) {
 }
 
 template <int HD, int NR>
-__global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
+__global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 : 3)
     narrow_kernel(const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p) {
   using CF = Narrow<HD, NR>;
@@ -927,7 +954,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 16 ? 2 : 1)
   griddep_wait();
   const Batch& bt = p.bt;
   const int g = static_cast<int>(blockIdx.x) % p.Hkv;
-  const int b = static_cast<int>(blockIdx.x) / p.Hkv;
+  const int bx = static_cast<int>(blockIdx.x) / p.Hkv;
+  const int b = p.sorted ? nth_longest(bt, bx, reinterpret_cast<int*>(sP), NARROW_THREADS) : bx;
   const int split = blockIdx.y;
   const Seq s = load_seq(bt, b, p.max_prefix, 0x511, threadIdx.x == 0 && split == 0 && g == 0);
   const int rows = s.n * p.group;
