@@ -302,14 +302,19 @@ class PagedCache:
     codes) and k_exp, v_exp uint8 [n_pages, Hkv] (a page's scale is 2^(exp - 127))."""
 
     def __init__(self, k_pages, v_pages, k_exp, v_exp):
-        for t in (k_pages, v_pages, k_exp, v_exp):
-            if t.dtype != torch.uint8:
-                raise ValueError("codes and exponents must be uint8")
+        tensors = (k_pages, v_pages, k_exp, v_exp)
+        if any(t.dtype != torch.uint8 for t in tensors):
+            raise ValueError("codes and exponents must be uint8")
         if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or \
                 k_exp.shape != k_pages.shape[:2] or v_exp.shape != k_exp.shape:
             raise ValueError("pages must be [n_pages, Hkv, page, hd], exponents [n_pages, Hkv]")
-        _need_contig(k_pages, v_pages, k_exp, v_exp)
-        self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
+        if any(t.device != k_pages.device for t in tensors):
+            raise ValueError("codes and exponents must be on one device")
+        _need_contig(*tensors)
+        self.k_pages, self.v_pages, self.k_exp, self.v_exp = tensors
+        self.n_pages, self.n_kv_heads, self.page, self.head_dim = k_pages.shape
+        self.device_index = k_pages.get_device()
+        self.pointers = tuple(t.data_ptr() for t in tensors)  # the tensors above keep them valid
 
     @classmethod
     def zeros(cls, n_pages, n_kv_heads, page, head_dim, device="cuda"):
@@ -328,27 +333,41 @@ def rope_table(n_positions, rot_dim, base=10000.0, device="cuda"):
     return torch.stack([angle.cos(), angle.sin()], -1).float().contiguous()
 
 
-def _rows(t, name, dtype=torch.bfloat16):
-    """Row stride of a packed [T, ld] tensor."""
-    if t.dtype != dtype or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be [T, ld] {dtype} with unit inner stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+# The paged calls are made once per layer and generated token: their argument
+# marshalling is on the latency path, so it asks torch for as little as it can.
+_BF16, _INT32, _FLOAT32 = torch.bfloat16, torch.int32, torch.float32
 
 
-def _paged_batch(cache, page_table, tok_start, cache_len, others):
-    """Checks of the index tensors that append and attention share."""
+def _raw_stream(stream, dev):
+    """The cudaStream_t of `stream`, or of the device's current one, as an integer."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _rows(t, name, dev, rows, cols):
+    """(row stride, device pointer) of a packed bf16 tensor [rows, >= cols]."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != _BF16 or len(shape) != 2 or shape[0] != rows or shape[1] < cols or \
+            (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be [{rows}, >= {cols}] bf16 with unit inner stride")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+    return (stride[0] if rows > 1 else max(stride[0], shape[1])), t.data_ptr()
+
+
+def _paged_batch(cache, page_table, tok_start, cache_len):
+    """Checks of the index tensors that append and attention share; (B, max_pages, device)."""
+    dev = cache.device_index
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the cache must be on the current CUDA device")
     for t in (page_table, tok_start, cache_len):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError("page_table, tok_start and cache_len must be contiguous int32")
-    B = cache_len.shape[0]
-    if page_table.dim() != 2 or page_table.shape[0] != B or tok_start.shape != (B + 1,):
+        if t.dtype != _INT32 or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError("page_table, tok_start and cache_len must be contiguous int32 on the "
+                             "cache's device")
+    shape = page_table.shape
+    B = cache_len.numel()
+    if len(shape) != 2 or shape[0] != B or tok_start.numel() != B + 1:
         raise ValueError("page_table must be [B, max_pages], tok_start [B + 1], cache_len [B]")
-    dev = torch.cuda.current_device()
-    for t in (cache.k_pages, cache.v_pages, cache.k_exp, cache.v_exp, page_table, tok_start,
-              cache_len, *others):
-        if t is not None and t.device.index != dev:
-            raise ValueError("every tensor must be on the current CUDA device")
-    return B
+    return B, shape[1], dev
 
 
 def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, rope=None,
@@ -360,29 +379,35 @@ def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, ro
     on every sequence's new rows; rope [n, rot_dim / 2, 2] fp32 (rope_table) or None; q, q_out
     [T, Hq*hd] bf16, the queries and where their rotated values go (q_out may be q).
     """
-    n_pages, Hkv, page, hd = cache.k_pages.shape
-    B = _paged_batch(cache, page_table, tok_start, cache_len, (k, v, rope, q, q_out))
-    ldkv = _rows(k, "k")
-    T = k.shape[0]
+    B, max_pages, dev = _paged_batch(cache, page_table, tok_start, cache_len)
+    T, Hkv, hd = k.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return
-    if v.shape[0] != T or _rows(v, "v") != ldkv or k.shape[1] < Hkv * hd or v.shape[1] < Hkv * hd:
-        raise ValueError("k and v must be [T, >= Hkv*hd] and share a row stride")
-    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 3 or
-                             rope.shape[2] != 2 or not rope.is_contiguous()):
-        raise ValueError("rope must be contiguous fp32 [positions, rot_dim / 2, 2]")
-    Hq = ldq = ldqo = 0
+    ldkv, kp = _rows(k, "k", dev, T, Hkv * hd)
+    ldv, vp = _rows(v, "v", dev, T, Hkv * hd)
+    if ldv != ldkv:
+        raise ValueError("k and v must share a row stride")
+    rope_len = rot = rp = Hq = ldq = ldqo = 0
+    if rope is not None:
+        rope_len, half, two = rope.shape
+        if rope.dtype != _FLOAT32 or two != 2 or not rope.is_contiguous() or \
+                rope.get_device() != dev:
+            raise ValueError("rope must be contiguous fp32 [positions, rot_dim / 2, 2] on the "
+                             "cache's device")
+        rot, rp = 2 * half, rope.data_ptr()
+    qp = qop = None
     if q is not None and q_out is not None:
-        Hq = q.shape[1] // hd
-        ldq, ldqo = _rows(q, "q"), _rows(q_out, "q_out")
-        if q.shape[0] != T or q_out.shape != q.shape:
-            raise ValueError("q and q_out must be [T, Hq*hd]")
+        Hq = q.shape[-1] // hd
+        ldq, qp = _rows(q, "q", dev, T, hd)
+        ldqo, qop = _rows(q_out, "q_out", dev, T, Hq * hd)
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out go together")
+    k_pages, v_pages, k_exp, v_exp = cache.pointers
     _lib.check(_lib.load().dg_kv_append_e4m3(
-        _ptr(k), _ptr(v), ldkv, _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(rope),
-        rope.shape[0] if rope is not None else 0, 2 * rope.shape[1] if rope is not None else 0,
-        1 if interleaved else 0, _ptr(cache.k_pages), _ptr(cache.v_pages), _ptr(cache.k_exp),
-        _ptr(cache.v_exp), n_pages, page, _ptr(page_table), page_table.shape[1], _ptr(tok_start),
-        _ptr(cache_len), max_new, B, T, Hkv, hd, _stream(stream)))
+        kp, vp, ldkv, qp, ldq, qop, ldqo, Hq, rp or None, rope_len, rot, 1 if interleaved else 0,
+        k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, page_table.data_ptr(),
+        max_pages, tok_start.data_ptr(), cache_len.data_ptr(), max_new, B, T, Hkv, hd,
+        _raw_stream(stream, dev)))
 
 
 def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_prefix, out, *,
@@ -394,32 +419,33 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
     rows' own keys; max_prefix a bound on every cache_len.  ws: a Workspace of the caller's for
     this stream or graph; without one the call takes its scratch from torch's allocator.
     """
-    n_pages, Hkv, page, hd = cache.k_pages.shape
-    B = _paged_batch(cache, page_table, tok_start, cache_len, (q, out, lse))
-    ldq, ldo = _rows(q, "q"), _rows(out, "out")
-    T = q.shape[0]
+    B, max_pages, dev = _paged_batch(cache, page_table, tok_start, cache_len)
+    T, Hkv, hd = q.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return out
-    if out.shape[0] != T or q.shape[1] < n_q_heads * hd or out.shape[1] < n_q_heads * hd:
-        raise ValueError("q and out must be [T, >= Hq*hd]")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, n_q_heads) or
-                            not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [T, Hq]")
+    ldq, qp = _rows(q, "q", dev, T, n_q_heads * hd)
+    ldo, op = _rows(out, "out", dev, T, n_q_heads * hd)
+    zp = None
+    if lse is not None:
+        if lse.dtype != _FLOAT32 or lse.shape != (T, n_q_heads) or not lse.is_contiguous() or \
+                lse.get_device() != dev:
+            raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
+        zp = lse.data_ptr()
     lib = _lib.load()
     need = lib.dg_paged_attn_workspace_bytes(B, T, n_q_heads, Hkv, hd, max_new, max_prefix)
     wp, wn = None, 0
     if need and ws is not None:
         wp, wn = ws.args(need)
     elif need:
-        s = stream if stream is not None else torch.cuda.current_stream()
-        with torch.cuda.stream(s):
+        with torch.cuda.stream(stream):  # a no-op for None
             buf = torch.empty(need, dtype=torch.uint8, device=q.device)
-        wp, wn = _ptr(buf), need
+        wp, wn = buf.data_ptr(), need
+    k_pages, v_pages, k_exp, v_exp = cache.pointers
     _lib.check(lib.dg_paged_attn_e4m3(
-        _ptr(q), ldq, _ptr(cache.k_pages), _ptr(cache.v_pages), _ptr(cache.k_exp),
-        _ptr(cache.v_exp), n_pages, page, _ptr(page_table), page_table.shape[1], _ptr(tok_start),
-        _ptr(cache_len), max_new, max_prefix, _ptr(out), ldo, _ptr(lse), B, T, n_q_heads, Hkv, hd,
-        hd ** -0.5 if scale is None else scale, mask, wp, wn, _stream(stream)))
+        qp, ldq, k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, page_table.data_ptr(),
+        max_pages, tok_start.data_ptr(), cache_len.data_ptr(), max_new, max_prefix, op, ldo, zp, B,
+        T, n_q_heads, Hkv, hd, hd ** -0.5 if scale is None else scale, mask, wp, wn,
+        _raw_stream(stream, dev)))
     return out
 
 
