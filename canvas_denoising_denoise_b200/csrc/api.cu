@@ -683,9 +683,9 @@ int check_paged(const char* fn, int n_pages, int page, int max_pages, int B, int
 }
 
 template <int HD>
-int launch_append(const dg::paged::AppendParams& p, int blocks, cudaStream_t s) {
-  DG_CUDA(launch_ex(dg::paged::append_kernel<HD>, dim3(blocks), dim3(dg::paged::APPEND_THREADS), 0,
-                    s, 1, p));
+int launch_append(const dg::paged::AppendParams& p, dim3 grid, cudaStream_t s) {
+  DG_CUDA(launch_ex(dg::paged::append_kernel<HD>, grid, dim3(dg::paged::APPEND_THREADS), 0, s, 1,
+                    p));
   count_launch();
   DG_CUDA(cudaGetLastError());
   return DG_OK;
@@ -1739,17 +1739,14 @@ int dg_kv_append_e4m3(const void* k, const void* v, int ldkv, const void* q, int
   p.q_out = (__nv_bfloat16*)q_out;
   p.ldkv = ldkv; p.ldq = ldq; p.ldqo = ldqo;
   p.k_pages = k_pages; p.v_pages = v_pages; p.k_exp = k_exp; p.v_exp = v_exp;
-  p.slots = (p.bt.max_new + page - 2) / page + 1;
+  const long long slots = ((long long)p.bt.max_new + page - 2) / page + 1;
   p.kv_blocks = cdiv(2 * Hkv, dg::paged::APPEND_THREADS / (2 * page));
-  const long long items =
-      q ? (long long)p.bt.max_new * (hd / 16) * cdiv(Hq, dg::paged::Q_HEADS) : 0;
-  const long long q_blocks = (items + dg::paged::APPEND_THREADS - 1) / dg::paged::APPEND_THREADS;
-  const long long blocks = (long long)B * p.slots * p.kv_blocks + B * q_blocks;
-  if (blocks > 0x7FFFFFFFll || items > 0x7FFFFF00ll)
-    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: too many rows for one launch", fn);
-  p.q_blocks = (int)std::max(1ll, q_blocks);
-  return hd == 128 ? launch_append<128>(p, (int)blocks, (cudaStream_t)stream)
-                   : launch_append<64>(p, (int)blocks, (cudaStream_t)stream);
+  const int items = q ? cdiv(Hq, dg::paged::Q_HEADS) * (hd / 16) * page : 0;
+  if (slots > 65535 || Hkv > (1 << 20) || Hq > (1 << 16))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: more than 65535 pages per sequence", fn);
+  const dim3 grid(p.kv_blocks + cdiv(items, dg::paged::APPEND_THREADS), (unsigned)slots, B);
+  return hd == 128 ? launch_append<128>(p, grid, (cudaStream_t)stream)
+                   : launch_append<64>(p, grid, (cudaStream_t)stream);
 }
 
 size_t dg_paged_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int hd, int max_new,

@@ -110,19 +110,17 @@ __device__ __forceinline__ void rotate(float& x, float& y, float2 cs) {
   x = a;
 }
 
-// The two chunks of pair index i (8 pairs of elements); both layouts take the
-// angles of pairs 8 i .. 8 i + 7.
-__device__ __forceinline__ void rotate_chunks(float (&a)[8], float (&b)[8], const float2 (&cs)[8],
-                                              bool interleaved) {
+// Half h of the eight pairs that the chunks a and b of a pair index form: their
+// elements 4 h .. 4 h + 3 with each other, or the adjacent pairs of one chunk.
+__device__ __forceinline__ void rotate_half(float (&a)[8], float (&b)[8], const float2 (&cs)[4],
+                                            int h, bool interleaved) {
   if (interleaved) {
+    float(&x)[8] = h ? b : a;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      rotate(a[2 * j], a[2 * j + 1], cs[j]);
-      rotate(b[2 * j], b[2 * j + 1], cs[4 + j]);
-    }
+    for (int j = 0; j < 4; ++j) rotate(x[2 * j], x[2 * j + 1], cs[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rotate(a[j], b[j], cs[j]);
+    for (int j = 0; j < 4; ++j) rotate(a[4 * h + j], b[4 * h + j], cs[j]);
   }
 }
 
@@ -138,9 +136,7 @@ struct AppendParams {
   int ldkv, ldq, ldqo;
   uint8_t *k_pages, *v_pages;  // [n_pages, Hkv, page, hd]
   uint8_t *k_exp, *v_exp;      // [n_pages, Hkv]
-  int slots;      // pages that one sequence's new rows can touch
-  int kv_blocks;  // CTAs per (sequence, page slot)
-  int q_blocks;   // CTAs per sequence for the queries
+  int kv_blocks;  // CTAs per (sequence, page) for keys and values; further ones for queries
 };
 
 constexpr int APPEND_THREADS = 256;
@@ -158,158 +154,182 @@ __device__ __forceinline__ void chunk_pair(const AppendParams& p, int i, int* a,
   }
 }
 
-__device__ __forceinline__ void load_angles(const AppendParams& p, int pos, int i,
-                                            float2 (&cs)[8]) {
-  const float4* t = reinterpret_cast<const float4*>(p.rope + static_cast<size_t>(pos) * p.half) +
-                    4 * i;
+// Angles 4 h .. 4 h + 3 of pair index i's eight.
+__device__ __forceinline__ void load_angles(const AppendParams& p, int pos, int i, int h,
+                                            float2 (&cs)[4]) {
+  const float4* t = reinterpret_cast<const float4*>(p.rope + static_cast<int64_t>(pos) * p.half) +
+                    4 * i + 2 * h;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     const float4 f = __ldg(t + j);
     cs[2 * j] = make_float2(f.x, f.y);
     cs[2 * j + 1] = make_float2(f.z, f.w);
   }
 }
 
+// Grid: z = sequence, y = page that its new rows touch, x = units of that page
+// and then its rows' queries.  Every index below is a shift: at 16 elements a
+// thread, divisions would be most of the instructions.
 template <int HD>
-__global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(APPEND_THREADS, 3) append_kernel(const AppendParams p) {
   constexpr int PAIRS = HD / 16;  // chunk pairs per row
+  constexpr int LOG_PAIRS = HD == 128 ? 3 : 2;
   constexpr int ROWS = HD / 32;   // rows per thread of a unit
   __shared__ float red[APPEND_THREADS / 32];
   griddep_launch();
   griddep_wait();
   const Batch& bt = p.bt;
-  const int kv_total = bt.B * p.slots * p.kv_blocks;
-  const bool rotated = p.half > 0;
+  const int b = blockIdx.z;
+  const int slot = blockIdx.y;
+  const int blk = blockIdx.x;
+  const bool report = slot == 0 && blk == 0 && threadIdx.x == 0;
+  Seq s = load_seq(bt, b, INT_MAX, 0x501, report);
+  if (p.half > 0 && s.n > 0 && s.n > p.rope_len - s.c0) {
+    if (report) raise_error(ERR_CHECK | 0x502, b);
+    s.n = 0;
+  }
+  const int page_idx = (s.c0 >> bt.log_page) + slot;
+  const int base = page_idx << bt.log_page;  // position of the page's first row
+  // the page's rows [r_beg, r_end) are new
+  const int r_beg = max(s.c0 - base, 0);
+  const int r_end = min(s.c0 + s.n - base, bt.page);
+  if (s.n == 0 || r_beg >= r_end) return;
 
-  if (static_cast<int>(blockIdx.x) >= kv_total) {
+  if (blk >= p.kv_blocks) {
     // ------------------------------------------------------------ queries
-    const int x = static_cast<int>(blockIdx.x) - kv_total;
-    const int b = x / p.q_blocks;
-    const Seq s = load_seq(bt, b, INT_MAX, 0x501, false);
-    const int groups = (p.Hq + Q_HEADS - 1) / Q_HEADS;
-    const int item = (x % p.q_blocks) * APPEND_THREADS + static_cast<int>(threadIdx.x);
-    const int i = item % PAIRS;
-    const int hg = (item / PAIRS) % groups;
-    const int row = item / (PAIRS * groups);
-    if (row >= s.n || s.c0 + row >= p.rope_len) return;
+    const int item = (blk - p.kv_blocks) * APPEND_THREADS + static_cast<int>(threadIdx.x);
+    const int i = item & (PAIRS - 1);
+    const int r = (item >> LOG_PAIRS) & (bt.page - 1);
+    const int h0 = (item >> (LOG_PAIRS + bt.log_page)) * Q_HEADS;
+    if (r < r_beg || r >= r_end || h0 >= p.Hq) return;
     int ca, cb;
     chunk_pair(p, i, &ca, &cb);
-    const __nv_bfloat16* src = p.q + static_cast<size_t>(s.t0 + row) * p.ldq;
-    __nv_bfloat16* dst = p.q_out + static_cast<size_t>(s.t0 + row) * p.ldqo;
+    const int64_t row = s.t0 + base + r - s.c0;
+    const __nv_bfloat16* src = p.q + row * p.ldq + h0 * HD;
+    __nv_bfloat16* dst = p.q_out + row * p.ldqo + h0 * HD;
     const bool turn = i * 8 < p.half;
-    float2 cs[8];
-    if (turn) load_angles(p, s.c0 + row, i, cs);
-    const int h1 = min(p.Hq, (hg + 1) * Q_HEADS);
+    const int heads = min(Q_HEADS, p.Hq - h0);
+    uint4 ra[Q_HEADS], rb[Q_HEADS];
 #pragma unroll
     for (int u = 0; u < Q_HEADS; ++u) {
-      const int h = hg * Q_HEADS + u;
-      if (h >= h1) break;
-      const uint4 ra = *reinterpret_cast<const uint4*>(src + h * HD + ca * 8);
-      const uint4 rb = *reinterpret_cast<const uint4*>(src + h * HD + cb * 8);
-      uint4 wa = ra, wb = rb;
-      if (turn) {
-        float a[8], c[8];
-        unpack_bf16x8(ra, a);
-        unpack_bf16x8(rb, c);
-        rotate_chunks(a, c, cs, p.interleaved != 0);
-        wa = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                        pack_bf16x2(a[6], a[7]));
-        wb = make_uint4(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]), pack_bf16x2(c[4], c[5]),
-                        pack_bf16x2(c[6], c[7]));
+      if (u < heads) {
+        ra[u] = *reinterpret_cast<const uint4*>(src + u * HD + ca * 8);
+        rb[u] = *reinterpret_cast<const uint4*>(src + u * HD + cb * 8);
       }
-      *reinterpret_cast<uint4*>(dst + h * HD + ca * 8) = wa;
-      *reinterpret_cast<uint4*>(dst + h * HD + cb * 8) = wb;
+    }
+    if (turn) {
+      float2 cs[2][4];
+      load_angles(p, base + r, i, 0, cs[0]);
+      load_angles(p, base + r, i, 1, cs[1]);
+#pragma unroll
+      for (int u = 0; u < Q_HEADS; ++u) {
+        float a[8], c[8];
+        unpack_bf16x8(ra[u], a);
+        unpack_bf16x8(rb[u], c);
+        rotate_half(a, c, cs[0], 0, p.interleaved != 0);
+        rotate_half(a, c, cs[1], 1, p.interleaved != 0);
+        ra[u] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                           pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+        rb[u] = make_uint4(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]),
+                           pack_bf16x2(c[4], c[5]), pack_bf16x2(c[6], c[7]));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < Q_HEADS; ++u) {
+      if (u < heads) {
+        *reinterpret_cast<uint4*>(dst + u * HD + ca * 8) = ra[u];
+        *reinterpret_cast<uint4*>(dst + u * HD + cb * 8) = rb[u];
+      }
     }
     return;
   }
 
   // -------------------------------------------------------------- keys and values
-  const int b = static_cast<int>(blockIdx.x) / (p.slots * p.kv_blocks);
-  const int slot = (static_cast<int>(blockIdx.x) / p.kv_blocks) % p.slots;
-  const int blk = static_cast<int>(blockIdx.x) % p.kv_blocks;
-  Seq s = load_seq(bt, b, INT_MAX, 0x501, slot == 0 && blk == 0 && threadIdx.x == 0);
-  if (rotated && s.c0 + s.n > p.rope_len && s.n > 0) {
-    if (slot == 0 && blk == 0 && threadIdx.x == 0) raise_error(ERR_CHECK | 0x502, b);
-    s.n = 0;
-  }
-  const int page_idx = (s.c0 >> bt.log_page) + slot;
-  const int base = page_idx << bt.log_page;  // position of the page's first row
-  if (s.n == 0 || base >= s.c0 + s.n) return;
-  const int pg = bt.page_table[static_cast<size_t>(b) * bt.max_pages + page_idx];
+  const int pg = bt.page_table[static_cast<int64_t>(b) * bt.max_pages + page_idx];
   if (pg < 0 || pg >= bt.n_pages) {
     if (blk == 0 && threadIdx.x == 0) raise_error(ERR_CHECK | 0x503, b);
     return;
   }
-
-  const int threads = 2 * bt.page;  // of one unit
-  const int unit = blk * (APPEND_THREADS / threads) + static_cast<int>(threadIdx.x) / threads;
+  const int log_threads = bt.log_page + 1;  // of one unit: 2 page
+  const int unit = (blk << (8 - log_threads)) + (static_cast<int>(threadIdx.x) >> log_threads);
   const bool live = unit < 2 * p.Hkv;
   const bool is_v = unit >= p.Hkv;
   const int g = live ? (is_v ? unit - p.Hkv : unit) : 0;
-  const int tu = static_cast<int>(threadIdx.x) % threads;
-  const int i = tu % PAIRS;
-  const int row0 = tu / PAIRS;
-  const int row_step = threads / PAIRS;
+  const int tu = static_cast<int>(threadIdx.x) & ((1 << log_threads) - 1);
+  const int i = tu & (PAIRS - 1);
+  const int row0 = tu >> LOG_PAIRS;
+  const int row_step = 1 << (log_threads - LOG_PAIRS);
   int ca, cb;
   chunk_pair(p, i, &ca, &cb);
-  const __nv_bfloat16* src = (is_v ? p.v : p.k) + static_cast<size_t>(g) * HD;
-  const size_t head = static_cast<size_t>(pg) * p.Hkv + g;
+  const __nv_bfloat16* src =
+      (is_v ? p.v : p.k) + static_cast<int64_t>(s.t0 + base - s.c0) * p.ldkv + g * HD;
+  const int64_t head = static_cast<int64_t>(pg) * p.Hkv + g;
   uint8_t* dst = (is_v ? p.v_pages : p.k_pages) + (head << bt.log_page) * HD;
   uint8_t* exp_at = (is_v ? p.v_exp : p.k_exp) + head;
-  const bool keeps = base < s.c0;  // rows of earlier appends stay in this page
+  const bool keeps = r_beg > 0;  // rows of earlier appends stay in this page
   const int e_old = keeps ? min(static_cast<int>(*exp_at) - 127, SCALE_MAX) : SCALE_MIN;
 
   uint4 ra[ROWS], rb[ROWS];
 #pragma unroll
   for (int u = 0; u < ROWS; ++u) {
-    const int pos = base + row0 + u * row_step;
+    const int r = row0 + u * row_step;
     ra[u] = rb[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && pos >= s.c0 && pos < s.c0 + s.n) {
-      const __nv_bfloat16* r = src + static_cast<size_t>(s.t0 + pos - s.c0) * p.ldkv;
-      ra[u] = *reinterpret_cast<const uint4*>(r + ca * 8);
-      rb[u] = *reinterpret_cast<const uint4*>(r + cb * 8);
+    if (live && r >= r_beg && r < r_end) {
+      const __nv_bfloat16* at = src + static_cast<int64_t>(r) * p.ldkv;
+      ra[u] = *reinterpret_cast<const uint4*>(at + ca * 8);
+      rb[u] = *reinterpret_cast<const uint4*>(at + cb * 8);
     }
   }
   float a[ROWS][8], c[ROWS][8];
   float amax = 0.f;
+  const bool turn = !is_v && i * 8 < p.half;
 #pragma unroll
   for (int u = 0; u < ROWS; ++u) {
-    const int pos = base + row0 + u * row_step;
+    const int r = row0 + u * row_step;
     unpack_bf16x8(ra[u], a[u]);
     unpack_bf16x8(rb[u], c[u]);
-    if (!is_v && i * 8 < p.half && pos >= s.c0 && pos < s.c0 + s.n) {
-      float2 cs[8];
-      load_angles(p, pos, i, cs);
-      rotate_chunks(a[u], c[u], cs, p.interleaved != 0);
+    if (turn && r >= r_beg && r < r_end) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 cs[4];
+        load_angles(p, base + r, i, h, cs);
+        rotate_half(a[u], c[u], cs, h, p.interleaved != 0);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = fabsf(a[u][e]), y = fabsf(c[u][e]);
-      amax = fmaxf(amax, x <= FLT_MAX ? x : 0.f);
-      amax = fmaxf(amax, y <= FLT_MAX ? y : 0.f);
-    }
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[u][e]), fabsf(c[u][e])));
   }
+  if (!(amax <= FLT_MAX)) {  // infinities are left out (the maximum drops NaN by itself)
+    amax = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (threads > 32) {  // the same for every unit of the launch
+    for (int u = 0; u < ROWS; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = fabsf(a[u][e]), y = fabsf(c[u][e]);
+        amax = fmaxf(amax, fmaxf(x <= FLT_MAX ? x : 0.f, y <= FLT_MAX ? y : 0.f));
+      }
+  }
+  // magnitudes order as their bits
+  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+  amax = __uint_as_float(top);
+  if (log_threads > 5) {  // the same for every unit of the launch
     if (lane_id() == 0) red[warp_id()] = amax;
     __syncthreads();
-    const int w0 = (static_cast<int>(threadIdx.x) / threads) * (threads / 32);
-    for (int w = 0; w < threads / 32; ++w) amax = fmaxf(amax, red[w0 + w]);
+    const int w0 = (static_cast<int>(threadIdx.x) >> log_threads) << (log_threads - 5);
+    for (int w = 0; w < 1 << (log_threads - 5); ++w) amax = fmaxf(amax, red[w0 + w]);
   }
   if (!live) return;
   const int e = max(scale_exponent(amax), e_old);
   const float f = pow2(-e);
 #pragma unroll
   for (int u = 0; u < ROWS; ++u) {
-    const int row = row0 + u * row_step;
-    const int pos = base + row;
-    uint2* da = reinterpret_cast<uint2*>(dst + static_cast<size_t>(row) * HD + ca * 8);
-    uint2* db = reinterpret_cast<uint2*>(dst + static_cast<size_t>(row) * HD + cb * 8);
-    if (pos >= s.c0 && pos < s.c0 + s.n) {
+    const int r = row0 + u * row_step;
+    uint2* da = reinterpret_cast<uint2*>(dst + r * HD + ca * 8);
+    uint2* db = reinterpret_cast<uint2*>(dst + r * HD + cb * 8);
+    if (r >= r_beg && r < r_end) {
       *da = pack_e4m3x8(a[u], f);
       *db = pack_e4m3x8(c[u], f);
-    } else if (pos < s.c0 && e > e_old) {
+    } else if (r < r_beg && e > e_old) {
       const float down = exp2f(static_cast<float>(e_old - e));
       float x[8];
       unpack_e4m3x8(*da, x);
