@@ -855,9 +855,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // codes as TMA delivered them: the kernel streams the cache and does nothing
 // else to it, and is bound by HBM once there are enough keys.
 //
-// The running maximum m is common to all keys of the CTA and only raised when
-// a score would pass 2^8.5 (p carries 2^4): the test costs one barrier with an
-// OR a tile, the raise itself (shuffles, rescaling O) is rare.
+// The running maximum m is common to all keys of the CTA; the first tile sets
+// it, and it is only raised when a score would pass 2^8.5 (p carries 2^4): the
+// test costs one barrier with an OR a tile, the raise itself is rare.
 //
 // Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer, 2..5 = softmax (thread
 // = key; at the end thread = element of the head).
@@ -915,10 +915,10 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
   uint8_t* sP = sV + ST * CF::T_BYTES;       // [128 keys][p0 | p1 | p2 | 0]
   uint8_t* sQ = sP + CF::P_BYTES;            // [NR hi rows][NR lo rows]
   float* sF = reinterpret_cast<float*>(sQ + CF::Q_BYTES);  // [NR] row factors
-  float* sM = sF + NR;                                     // [NR] running maxima (log2 units)
-  int* sSees = reinterpret_cast<int*>(sM + NR);            // [NR] visible keys
+  float* sM = sF + NR;                                     // [2][NR] running maxima (log2 units)
+  int* sSees = reinterpret_cast<int*>(sM + 2 * NR);        // [NR] visible keys
   float* sRed = reinterpret_cast<float*>(sSees + NR);      // [4][NR]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sRed + 5 * NR);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRed + 4 * NR);
   uint64_t* q_full = bars;
   uint64_t* k_full = q_full + 1;       // [ST]
   uint64_t* k_empty = k_full + ST;     // [ST]
@@ -930,6 +930,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
   uint64_t* drain = pv_done + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* s_fail = abort_flag + 1;  // a softmax thread gave up waiting
 
   const int warp = warp_id();
   const int lane = lane_id();
@@ -947,6 +948,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     mbar_init(pv_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *s_fail = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
   }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + NR) {
     const int r = static_cast<int>(threadIdx.x) - 64;
-    sM[r] = -INFINITY;
+    sM[r] = 0.f;
     sSees[r] = p.causal ? min(total, s.c0 + token_of(p, r) + 1) : total;
   }
   tc_fence_before();
@@ -986,7 +988,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
   const uint32_t tmem = *tmem_holder;
 
   if (idle) {
-    if (threadIdx.x < NR) sF[threadIdx.x] = 0.f;  // no weight; the maximum stays at -inf
+    if (threadIdx.x < NR) sF[threadIdx.x] = 0.f;  // no weight
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int ppt = 1 << log_ppt;
@@ -1110,6 +1112,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     for (int r = 0; r < NR; ++r) l[r] = 0.f;
     bar_any(1, 128, false);  // row factors are in place
     bool ok = true;
+    int cur = 0;  // which of sM holds the maxima
     int j = 0;
     for (; j < n; ++j) {
       const float kf = __uint_as_float(static_cast<uint32_t>(ke) << 23);
@@ -1127,36 +1130,39 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
                       ok && mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag, 0x581));
       tc_fence_after();
       float x[NR];
-      // x = score in log2 units + shift - (with_max ? running maximum : 0)
-      auto scores = [&](float shift, bool with_max) {
+      // x = score in log2 units + ev (the V scale) + shift - running maximum
+      const float* m_now = sM + cur * NR;
 #pragma unroll
-        for (int c = 0; c < NR; c += 16) {
-          uint32_t hi[16], lo[16];
-          tmem_ld16(tS + c, hi);
-          tmem_ld16(tS + NR + c, lo);
-          tmem_ld_wait();
+      for (int c = 0; c < NR; c += 16) {
+        uint32_t hi[16], lo[16];
+        tmem_ld16(tS + c, hi);
+        tmem_ld16(tS + NR + c, lo);
+        tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 16; q += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sF + c + q);
-            const float4 m = *reinterpret_cast<const float4*>(sM + c + q);
-            const float ff[4] = {f.x, f.y, f.z, f.w}, mm[4] = {m.x, m.y, m.z, m.w};
+        for (int q = 0; q < 16; q += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sF + c + q);
+          const float4 m = *reinterpret_cast<const float4*>(m_now + c + q);
+          const float ff[4] = {f.x, f.y, f.z, f.w}, mm[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float sum = __uint_as_float(hi[q + e]) + __uint_as_float(lo[q + e]);
-              x[c + q + e] = fmaf(sum, ff[e] * kf, with_max ? shift - mm[e] : shift);
-              if (edge && pos >= sSees[c + q + e]) x[c + q + e] = -INFINITY;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float sum = __uint_as_float(hi[q + e]) + __uint_as_float(lo[q + e]);
+            x[c + q + e] = fmaf(sum, ff[e] * kf, (ev + N_SHIFT) - mm[e]);
+            if (edge && pos >= sSees[c + q + e]) x[c + q + e] = -INFINITY;
           }
         }
-      };
-      scores(ev + N_SHIFT, true);
-      bool above = false;
+      }
+      bool raise = j == 0;  // the first tile sets the maxima without a test
+      if (j > 0) {
+        bool above = false;
 #pragma unroll
-      for (int r = 0; r < NR; ++r) above = above || x[r] > N_LIMIT;
-      if (bar_any(1, 128, above || !ok)) {
-        if (bar_any(1, 128, !ok || *abort_flag)) break;
+        for (int r = 0; r < NR; ++r) above = above || x[r] > N_LIMIT;
+        if (!ok) *s_fail = 1;
+        raise = bar_any(1, 128, above || !ok);
+      } else if (!ok) {
+        *s_fail = 1;
+      }
+      if (raise) {
         // raise the maxima to this tile's
-        scores(ev, false);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float v = warp_top(x[r]);
@@ -1167,19 +1173,26 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
           tc_fence_after();
         }
         bar_any(1, 128, false);
-        float mine = -INFINITY;
+        // s_fail is written before a barrier only, and read only behind the
+        // next: every thread sees the same
+        if (*s_fail) break;
+        float* m_next = sM + (cur ^ 1) * NR;
+        float mine = 0.f;
 #pragma unroll
         for (int c = 0; c < NR; c += 16) {
           float fac[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int r = c + e;
-            const float old = sM[r];
-            const float top = fmaxf(fmaxf(fmaxf(sRed[r], sRed[NR + r]),
-                                          fmaxf(sRed[2 * NR + r], sRed[3 * NR + r])), old);
-            fac[e] = old == -INFINITY ? 0.f : attn::fast_exp2(old - top);
+            // how far the tile's maximum lies above the running one; the first
+            // tile's becomes the running one either way, unless the row sees no key
+            const float d = fmaxf(fmaxf(sRed[r], sRed[NR + r]),
+                                  fmaxf(sRed[2 * NR + r], sRed[3 * NR + r])) - N_SHIFT;
+            const float up = d == -INFINITY ? 0.f : (j > 0 ? fmaxf(d, 0.f) : d);
+            fac[e] = attn::fast_exp2(-up);
             l[r] *= fac[e];
-            if (r == kl) mine = top;
+            x[r] -= up;
+            if (r == kl) mine = m_now[r] + up;
           }
           if (j > 0) {
 #pragma unroll
@@ -1195,10 +1208,9 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
           }
         }
         tmem_st_wait();
-        bar_any(1, 128, false);  // everyone has read the old maxima
-        if (kl < NR) sM[kl] = mine;
+        if (kl < NR) m_next[kl] = mine;
+        cur ^= 1;
         bar_any(1, 128, false);
-        scores(ev + N_SHIFT, true);
       }
       // P rows may be rewritten once the previous product has read them
       if (j > 0)
@@ -1251,6 +1263,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     ok = __all_sync(0xffffffffu, ok && j == n &&
                                      mbar_wait(pv_done, (n - 1) & 1, abort_flag, 0x585));
     tc_fence_after();
+    if (kl < NR && cur) sM[kl] = sM[NR + kl];
     // sum of l over the warp's 32 keys for all rows at once: each exchange
     // halves the rows that a lane still carries
 #pragma unroll
@@ -1349,13 +1362,14 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < MAX_CLUSTER; ++k) top = fmaxf(top, m[k]);
+        for (int k = 0; k < MAX_CLUSTER; ++k)
+          if (f[k] != 0.f) top = fmaxf(top, m[k]);
         float sum = 0.f, v = 0.f;
 #pragma unroll
         for (int k = 0; k < MAX_CLUSTER; ++k) {
           // a split without a visible key left its O unwritten
           if (f[k] != 0.f) {
-            const float e = m[k] == -INFINITY ? 1.f : attn::fast_exp2(m[k] - top);
+            const float e = attn::fast_exp2(m[k] - top);
             sum = fmaf(e, f[k], sum);
             v = fmaf(e, o[k], v);
           }
