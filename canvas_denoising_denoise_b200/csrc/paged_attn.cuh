@@ -95,6 +95,35 @@ __device__ __forceinline__ int swz(int r, int c) {
   return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+
+// Two fp32 operations in one instruction, and the largest of three values: the
+// softmax warps are bound by how many instructions they issue.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 struct AttnParams {
   Batch bt;
   int Hq, Hkv, group, causal;
@@ -688,16 +717,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         for (int c = 0; c < 128; ++c)
           if (c > lim) sa[c] = __float_as_uint(-INFINITY);
       }
-      // 32 keys from column c0: P as packed f16 pairs, their sum added to rs
-      float rs[4] = {0.f, 0.f, 0.f, 0.f};
+      // 32 keys' probabilities as packed f16 pairs, their sums added to rs
+      uint64_t rs[2] = {0, 0};
       auto probs = [&](const uint32_t* x, float f0, float f1, float neg_m, uint32_t* pk) {
+        const uint64_t m2 = pack2(neg_m, neg_m);
+        const uint64_t ff[2] = {pack2(f0, f0), pack2(f1, f1)};
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float f = c < 8 ? f0 : f1;
-          const float p0 = attn::fast_exp2(fmaf(__uint_as_float(x[2 * c]), f, neg_m));
-          const float p1 = attn::fast_exp2(fmaf(__uint_as_float(x[2 * c + 1]), f, neg_m));
-          rs[(2 * c) & 3] += p0;
-          rs[(2 * c + 1) & 3] += p1;
+          const float2 e = unpack2(fma2(pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])),
+                                        ff[c >> 3], m2));
+          const float p0 = attn::fast_exp2(e.x), p1 = attn::fast_exp2(e.y);
+          rs[c & 1] = add2(rs[c & 1], pack2(p0, p1));
           const __half2 a = __floats2half2_rn(p0, p1);
           pk[c] = *reinterpret_cast<const uint32_t*>(&a);
         }
@@ -717,10 +747,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           for (int q = 4 * h; q < 4 * h + 4; ++q) {
             float m0 = __uint_as_float(sa[16 * q]), m1 = __uint_as_float(sa[16 * q + 1]);
 #pragma unroll
-            for (int c = 2; c < 16; c += 2) {
-              m0 = fmaxf(m0, __uint_as_float(sa[16 * q + c]));
-              m1 = fmaxf(m1, __uint_as_float(sa[16 * q + c + 1]));
+            for (int c = 2; c < 14; c += 4) {
+              m0 = max3(m0, __uint_as_float(sa[16 * q + c]), __uint_as_float(sa[16 * q + c + 1]));
+              m1 = max3(m1, __uint_as_float(sa[16 * q + c + 2]), __uint_as_float(sa[16 * q + c + 3]));
             }
+            m0 = max3(m0, __uint_as_float(sa[16 * q + 14]), __uint_as_float(sa[16 * q + 15]));
             tmax = fmaxf(tmax, fmaxf(m0, m1) * scg[q]);
           }
         }
@@ -745,7 +776,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         }
         m = m_new;
         const float neg_m = (m == -INFINITY) ? 0.f : P_SHIFT - m;
-        rs[0] = rs[1] = rs[2] = rs[3] = 0.f;
+        rs[0] = rs[1] = 0;
         probs(&sa[0], scg[0], scg[1], neg_m, &pk[0]);
         probs(&sa[32], scg[2], scg[3], neg_m, &pk[16]);
       }
@@ -761,7 +792,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[2 * X + 1]);
-      l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+      const float2 sum = unpack2(add2(rs[0], rs[1]));
+      l += sum.x + sum.y;
     }
     const bool fin = __all_sync(0xffffffffu, ok && mbar_wait(o_final, 0, abort_flag, 0x553));
     // Stage O_X in the idle rings (rows XOR-swizzled by 16-byte chunk), then
@@ -1398,10 +1430,10 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
 // w_s = 2^(lse_s - max).  A warp per (token, head); only the splits that the
 // row's visible keys reach were written, and only those are read, in order.
 // ---------------------------------------------------------------------------
-// Lane s reads split s's log-sum-exp, so every weight is known after one load;
-// the partial rows then come COMBINE_BATCH at a time, none waiting for another.
+// Lane s reads split s's log-sum-exp, so every weight is known after one load,
+// beside which the first COMBINE_BATCH partial rows are already on their way.
 constexpr int COMBINE_THREADS = 256;
-constexpr int COMBINE_BATCH = 8;
+constexpr int COMBINE_BATCH = 12;
 
 template <int HD>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnParams p) {
@@ -1423,22 +1455,9 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnPara
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
   for (int s0 = 0; s0 < S; s0 += 32) {
-    const float z = s0 + lane < S ? p.part_lse[(s0 + lane) * stride + row] : -INFINITY;
-    float top = z;
-    bool bad = z != z;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = fmaxf(top, mx);
-    const float f = mx == -INFINITY ? 0.f : expf(mx - top);
-    // a split without a visible key weighs nothing; a NaN one makes the row NaN
-    const float w = z == -INFINITY ? 0.f : bad ? z : expf(z - top);
-    wsum = wsum * f + warp_sum(w);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] *= f;
-    mx = top;
     const int here = min(32, S - s0);
-    for (int k0 = 0; k0 < here; k0 += COMBINE_BATCH) {
-      float v[COMBINE_BATCH][PER];
+    float v[COMBINE_BATCH][PER];
+    auto load = [&](int k0) {
 #pragma unroll
       for (int k = 0; k < COMBINE_BATCH; ++k) {
         const float* src = p.part_o + ((s0 + k0 + k) * stride + row) * HD + lane * PER;
@@ -1450,6 +1469,19 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnPara
           v[k][e + 1] = x.y;
         }
       }
+    };
+    load(0);  // in flight beside the log-sum-exps
+    const float z = lane < here ? p.part_lse[(s0 + lane) * stride + row] : -INFINITY;
+    const float top = fmaxf(warp_top(z), mx);
+    const float f = mx == -INFINITY ? 0.f : expf(mx - top);
+    // a split without a visible key weighs nothing; a NaN one makes the row NaN
+    const float w = z == -INFINITY ? 0.f : z != z ? z : expf(z - top);
+    wsum = wsum * f + warp_sum(w);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= f;
+    mx = top;
+    for (int k0 = 0; k0 < here; k0 += COMBINE_BATCH) {
+      if (k0 > 0) load(k0);
 #pragma unroll
       for (int k = 0; k < COMBINE_BATCH; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
