@@ -911,6 +911,14 @@ struct Narrow {
   // A and B both M/N-major; the M = 128 lanes beyond a head of 64 are unused
   static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(128, 4 * NR) | (1u << 15) | (1u << 16);
   static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024 || NR > 16, "two CTAs per SM");
+  // Padding rows are left out from a few places on only: a test every four rows
+  // would keep the rows' instructions apart (32 rows: 38 -> 45 us).
+  static __device__ __forceinline__ bool stops(int r, int rows) {
+    return (NR == 16 ? r == 4 || r == 8 : r == 24) && r >= rows;
+  }
+  static __device__ __forceinline__ bool skips(int r, int rows) {
+    return NR == 16 ? (r >= 8 ? rows <= 8 : r >= 4 && rows <= 4) : r >= 24 && rows <= 24;
+  }
 };
 
 // OR of a predicate over the named barrier's threads.
@@ -1164,6 +1172,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
       float x[NR];
       // x = score in log2 units + ev (the V scale) + shift - running maximum
       const float* m_now = sM + cur * NR;
+      bool above = false;
 #pragma unroll
       for (int c = 0; c < NR; c += 16) {
         uint32_t hi[16], lo[16];
@@ -1172,6 +1181,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         tmem_ld_wait();
 #pragma unroll
         for (int q = 0; q < 16; q += 4) {
+          if (CF::stops(c + q, rows)) break;
           const float4 f = *reinterpret_cast<const float4*>(sF + c + q);
           const float4 m = *reinterpret_cast<const float4*>(m_now + c + q);
           const float ff[4] = {f.x, f.y, f.z, f.w}, mm[4] = {m.x, m.y, m.z, m.w};
@@ -1180,14 +1190,12 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
             const float sum = __uint_as_float(hi[q + e]) + __uint_as_float(lo[q + e]);
             x[c + q + e] = fmaf(sum, ff[e] * kf, (ev + N_SHIFT) - mm[e]);
             if (edge && pos >= sSees[c + q + e]) x[c + q + e] = -INFINITY;
+            above = above || x[c + q + e] > N_LIMIT;
           }
         }
       }
       bool raise = j == 0;  // the first tile sets the maxima without a test
       if (j > 0) {
-        bool above = false;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) above = above || x[r] > N_LIMIT;
         if (!ok) *s_fail = 1;
         raise = bar_any(1, 128, above || !ok);
       } else if (!ok) {
@@ -1196,9 +1204,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
       if (raise) {
         // raise the maxima to this tile's
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float v = warp_top(x[r]);
-          if (lane == 0) sRed[quarter * NR + r] = v;
+        for (int r = 0; r < NR; r += 4) {
+          if (CF::stops(r, rows)) break;
+          const float4 v = make_float4(warp_top(x[r]), warp_top(x[r + 1]), warp_top(x[r + 2]),
+                                       warp_top(x[r + 3]));
+          if (lane == 0) *reinterpret_cast<float4*>(sRed + quarter * NR + r) = v;
         }
         if (j > 0) {
           ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (j - 1) & 1, abort_flag, 0x582));
@@ -1216,6 +1226,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int r = c + e;
+            fac[e] = 1.f;
+            if (CF::skips(r, rows)) continue;
             // how far the tile's maximum lies above the running one; the first
             // tile's becomes the running one either way, unless the row sees no key
             const float d = fmaxf(fmaxf(sRed[r], sRed[NR + r]),
@@ -1249,9 +1261,10 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (j - 1) & 1, abort_flag, 0x583));
 #pragma unroll
       for (int c = 0; c < NR; c += 16) {
-        uint32_t w[3][4];
+        uint32_t w[3][4] = {};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          if (CF::stops(c + 4 * q, rows)) break;
           uint32_t term[3][2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
