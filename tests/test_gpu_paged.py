@@ -434,3 +434,113 @@ def test_wrapper_refuses():
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+@pytest.mark.parametrize("B,hkv,group,n", [(48, 8, 2, 1), (24, 8, 2, 40), (300, 1, 2, 1)])
+def test_attention_of_more_sequences_than_fit_at_once(B, hkv, group, n):
+    """CTAs that outnumber the SMs' slots, over lengths in no order (some sequences idle)."""
+    rng = np.random.default_rng(B)
+    lengths = [(0 if b % 11 == 5 else n, int(rng.integers(0, 400))) for b in range(B)]
+    check_attention(Case(lengths, hkv, group, 64, 32, seed=B), True)
+
+
+def test_pages_behind_two_gigabytes():
+    """Page ids whose codes lie past 2^31 and 2^32 bytes."""
+    d = dg()
+    case = Case([(3, 130), (40, 100), (1, 500)], 8, 2, 128, 128, seed=51)
+    small = case.cache
+    far = 33000  # pages of 128 KB: 4.3 GB of codes each for K and V
+    shift = far - case.n_pages
+    pages = [torch.zeros((far, 8, 128, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    exps = [torch.full((far, 8), 127, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for t, name in zip(pages + exps, ("k", "v", "k_exp", "v_exp")):
+        t[shift:] = torch.from_numpy(small[name]).cuda()
+    cache = d.PagedCache(pages[0], pages[1], exps[0], exps[1])
+    table = torch.from_numpy(np.where(case.table >= 0, case.table + shift, -1).astype(np.int32)).cuda()
+    starts, lens = torch.from_numpy(case.tok_start).cuda(), torch.from_numpy(case.cache_len).cuda()
+    q, k, v = case.q.cuda(), case.k.cuda(), case.v.cuda()
+    out = torch.full((case.T, 16 * 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    d.kv_append_e4m3(k, v, cache, table, starts, lens, case.max_new)
+    d.paged_attn_e4m3(q, cache, table, starts, lens, case.max_new, case.max_prefix, out,
+                      n_q_heads=16, mask=d.MASK_CAUSAL)
+    torch.cuda.synchronize()
+    d.check_device_errors()
+    paged.append(small, case.seqs, case.heads("k"), case.heads("v"))
+    for t, name in zip(pages + exps, ("k", "v", "k_exp", "v_exp")):
+        assert np.array_equal(t[shift:].cpu().numpy() & 0x7F, small[name] & 0x7F), name
+        assert int(t[:shift].max()) in (0, 127)
+    compare(case, out, None, True, 128 ** -0.5)
+
+
+def test_two_captured_graphs_do_not_share_scratch():
+    """Two graphs captured without a workspace, replayed at the same time on two streams."""
+    d = dg()
+    cases = [Case([(60, 1500)], 1, 2, 128, 64, seed=61), Case([(1, 5000)], 2, 2, 128, 64, seed=62)]
+    runs = []
+    for case in cases:
+        dev = case.device()
+        q = case.q.cuda()
+        out = torch.zeros((case.T, case.hq * 128), dtype=torch.bfloat16, device="cuda")
+
+        def call(dev=dev, q=q, out=out, case=case):
+            d.paged_attn_e4m3(q, *dev, case.max_new, case.max_prefix, out, n_q_heads=case.hq,
+                              mask=d.MASK_CAUSAL)
+
+        call()
+        torch.cuda.synchronize()
+        want = out.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, out, want, torch.cuda.Stream(), dev, q))
+    for _ in range(20):
+        for graph, out, _, stream, _, _ in runs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for graph, _, _, stream, _, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _, _, _ in runs:
+            assert torch.equal(out, want)
+    d.check_device_errors()
+
+
+def test_nan_codes_reach_the_rows_that_see_them():
+    d = dg()
+    for n in (2, 300):
+        case = Case([(n, 60), (n, 61)], 1, 2, 64, 16, seed=63)
+        pages = case.seqs[0][3]
+        case.cache["v"][pages[0], 0, 3, 5] = 0x7F  # position 3 of the first sequence, element 5
+        cache, table, starts, lens = case.device()
+        out = torch.zeros((case.T, 128), dtype=torch.bfloat16, device="cuda")
+        d.paged_attn_e4m3(case.q.cuda(), cache, table, starts, lens, n, 61, out, n_q_heads=2,
+                          mask=d.MASK_CAUSAL)
+        bad = out.float().isnan()
+        assert bad[:n, [5, 69]].all() and int(bad.sum()) == 2 * n
+
+
+def test_append_and_attention_on_two_streams_at_once():
+    """Two batches with their own caches, in flight together."""
+    d = dg()
+    cases = [Case([(64, 300), (200, 17)], 2, 2, 128, 32, seed=71),
+             Case([(1, 900)] * 9, 2, 4, 128, 64, seed=72)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    state = []
+    for case in cases:
+        dev = case.device()
+        state.append((case, dev, case.q.cuda(), case.k.cuda(), case.v.cuda(), rope_for(case, 128),
+                      torch.zeros((case.T, case.hq * 128), dtype=torch.bfloat16, device="cuda"),
+                      torch.zeros((case.T, case.hq * 128), dtype=torch.bfloat16, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for stream, (case, dev, q, k, v, rope, turned, out) in zip(streams, state):
+            d.kv_append_e4m3(k, v, *dev, case.max_new, rope=rope, q=q, q_out=turned, stream=stream)
+            d.paged_attn_e4m3(turned, *dev, case.max_new, case.max_prefix, out, n_q_heads=case.hq,
+                              mask=d.MASK_CAUSAL, stream=stream)
+    torch.cuda.synchronize()
+    d.check_device_errors()
+    for case, dev, q, k, v, rope, turned, out in state:
+        paged.append(case.cache, case.seqs, case.heads("k"), case.heads("v"), rope.cpu().numpy())
+        compare(case, out, None, True, 128 ** -0.5,
+                q=turned.float().cpu().numpy().reshape(case.T, case.hq, 128).astype(np.float64))
