@@ -697,6 +697,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const float sc = ok ? sQf[X * BQ + r] : 0.f;
     // keys [0, sees) are visible to this row
     const int sees = p.causal ? min(total, s.c0 + token_of(p, qrow) + 1) : total;
+    // keys [0, open_keys) are visible to every row of the CTA
+    const int open_keys = p.causal ? s.c0 + token_of(p, first) + 1 : total;
     for (int j = 0; j < n && ok; ++j) {
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[X], j & 1, abort_flag, 0x551))) {
         ok = false;
@@ -711,8 +713,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
       for (int q = 0; q < 8; ++q) scg[q] = sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)];
       const int lim = sees - (t_beg + j) * BKV - 1;  // columns [0, lim] are visible
+      const bool edge = (t_beg + j + 1) * BKV > open_keys;
       tmem_ld_wait();
-      if (__any_sync(0xffffffffu, lim < BKV - 1)) {
+      if (edge) {
 #pragma unroll
         for (int c = 0; c < 128; ++c)
           if (c > lim) sa[c] = __float_as_uint(-INFINITY);
@@ -777,8 +780,19 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         m = m_new;
         const float neg_m = (m == -INFINITY) ? 0.f : P_SHIFT - m;
         rs[0] = rs[1] = 0;
-        probs(&sa[0], scg[0], scg[1], neg_m, &pk[0]);
-        probs(&sa[32], scg[2], scg[3], neg_m, &pk[16]);
+        // (from TMEM again: kept in registers, the scores would cost spills)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t again[32];
+          tmem_ld32(tS + h * 32, again);
+          tmem_ld_wait();
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (h * 32 + c > lim) again[c] = __float_as_uint(-INFINITY);
+          }
+          probs(again, scg[2 * h], scg[2 * h + 1], neg_m, &pk[16 * h]);
+        }
       }
       // P takes the first half of S's columns
       tmem_st32(tS, pk);
