@@ -700,6 +700,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     // keys [0, open_keys) are visible to every row of the CTA
     const int open_keys = p.causal ? s.c0 + token_of(p, first) + 1 : total;
     for (int j = 0; j < n && ok; ++j) {
+      float scg[8];  // row factor times the page scale, per 16 columns
+#pragma unroll
+      for (int q = 0; q < 8; ++q) scg[q] = sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)];
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[X], j & 1, abort_flag, 0x551))) {
         ok = false;
         break;
@@ -709,9 +712,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         tmem_ld32(tS + h * 32, *reinterpret_cast<uint32_t(*)[32]>(&sa[32 * h]));
-      float scg[8];  // row factor times the page scale, per 16 columns
-#pragma unroll
-      for (int q = 0; q < 8; ++q) scg[q] = sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)];
       const int lim = sees - (t_beg + j) * BKV - 1;  // columns [0, lim] are visible
       const bool edge = (t_beg + j + 1) * BKV > open_keys;
       tmem_ld_wait();
