@@ -21,6 +21,12 @@
 // rotate with each other, so a rotation needs no exchange.  Queries are
 // rotated by further CTAs of the same launch; a thread keeps one row's angles
 // for several heads.
+//
+// Bound by HBM for long prompts: four of up to 4096 rows (8 kv and 16 query
+// heads of 128) in 35 us, 4.4 TB/s, 66% of the measured copy rate, with a third
+// of the SM's warps resident (80 registers: the rows are held in fp32) and 44%
+// of its issue slots taken by conversions and rotation.  Canvases and single
+// tokens are launch and latency: 4 to 9 us.
 #pragma once
 
 #include <cuda_fp8.h>
