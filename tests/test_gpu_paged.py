@@ -196,7 +196,8 @@ def test_attention_few_rows(hd, page, causal):
 
 
 @pytest.mark.parametrize("hkv,group,n", [(1, 1, 1), (3, 1, 300), (1, 7, 40), (2, 16, 1), (1, 32, 2),
-                                         (1, 20, 3), (8, 2, 1), (1, 3, 171)])
+                                         (1, 20, 3), (8, 2, 1), (1, 3, 171), (1, 32, 1),
+                                         (2, 3, 9), (1, 128, 2), (2, 25, 1)])
 def test_attention_groups(hkv, group, n):
     check_attention(Case([(n, 200), (max(1, n - 1), 5)], hkv, group, 128, 32, seed=group), True)
     check_attention(Case([(n, 391)], hkv, group, 64, 16, seed=group), False)
