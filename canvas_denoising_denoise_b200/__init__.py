@@ -344,30 +344,38 @@ def _raw_stream(stream, dev):
 
 
 def _rows(t, name, dev, rows, cols):
-    """(row stride, device pointer) of a packed bf16 tensor [rows, >= cols]."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != _BF16 or len(shape) != 2 or shape[0] != rows or shape[1] < cols or \
-            (stride[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be [{rows}, >= {cols}] bf16 with unit inner stride")
+    """(row stride, columns, device pointer) of a packed bf16 tensor [rows, >= cols]."""
+    shape = t.shape
+    if t.dtype is not _BF16 or len(shape) != 2:
+        raise ValueError(f"{name} must be a bf16 matrix")
+    n, width = shape
+    ld, inner = t.stride()
+    if n != rows or width < cols or (inner != 1 and width > 1):
+        raise ValueError(f"{name} must be [{rows}, >= {cols}] with unit inner stride")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the cache's device")
-    return (stride[0] if rows > 1 else max(stride[0], shape[1])), t.data_ptr()
+    return (ld if n > 1 or ld > width else width), width, t.data_ptr()
+
+
+def _index(t, name, dev):
+    """Device pointer of a contiguous int32 tensor."""
+    if t.dtype is not _INT32 or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be contiguous int32 on the cache's device")
+    return t.data_ptr()
 
 
 def _paged_batch(cache, page_table, tok_start, cache_len):
-    """Checks of the index tensors that append and attention share; (B, max_pages, device)."""
+    """The index tensors that append and attention share: their pointers, B and max_pages."""
     dev = cache.device_index
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("the cache must be on the current CUDA device")
-    for t in (page_table, tok_start, cache_len):
-        if t.dtype != _INT32 or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError("page_table, tok_start and cache_len must be contiguous int32 on the "
-                             "cache's device")
-    shape = page_table.shape
-    B = cache_len.numel()
+    pt = _index(page_table, "page_table", dev)
+    ts = _index(tok_start, "tok_start", dev)
+    cl = _index(cache_len, "cache_len", dev)
+    shape, B = page_table.shape, cache_len.numel()
     if len(shape) != 2 or shape[0] != B or tok_start.numel() != B + 1:
         raise ValueError("page_table must be [B, max_pages], tok_start [B + 1], cache_len [B]")
-    return B, shape[1], dev
+    return pt, ts, cl, B, shape[1], dev
 
 
 def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, rope=None,
@@ -379,35 +387,38 @@ def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, ro
     on every sequence's new rows; rope [n, rot_dim / 2, 2] fp32 (rope_table) or None; q, q_out
     [T, Hq*hd] bf16, the queries and where their rotated values go (q_out may be q).
     """
-    B, max_pages, dev = _paged_batch(cache, page_table, tok_start, cache_len)
+    pt, ts, cl, B, max_pages, dev = _paged_batch(cache, page_table, tok_start, cache_len)
     T, Hkv, hd = k.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return
-    ldkv, kp = _rows(k, "k", dev, T, Hkv * hd)
-    ldv, vp = _rows(v, "v", dev, T, Hkv * hd)
+    ldkv, _, kp = _rows(k, "k", dev, T, Hkv * hd)
+    ldv, _, vp = _rows(v, "v", dev, T, Hkv * hd)
     if ldv != ldkv:
         raise ValueError("k and v must share a row stride")
-    rope_len = rot = rp = Hq = ldq = ldqo = 0
+    rope_len = rot = Hq = ldq = ldqo = 0
+    rp = qp = qop = None
     if rope is not None:
         rope_len, half, two = rope.shape
-        if rope.dtype != _FLOAT32 or two != 2 or not rope.is_contiguous() or \
+        if rope.dtype is not _FLOAT32 or two != 2 or not rope.is_contiguous() or \
                 rope.get_device() != dev:
             raise ValueError("rope must be contiguous fp32 [positions, rot_dim / 2, 2] on the "
                              "cache's device")
         rot, rp = 2 * half, rope.data_ptr()
-    qp = qop = None
-    if q is not None and q_out is not None:
-        Hq = q.shape[-1] // hd
-        ldq, qp = _rows(q, "q", dev, T, hd)
-        ldqo, qop = _rows(q_out, "q_out", dev, T, Hq * hd)
-    elif q is not None or q_out is not None:
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q and q_out go together")
+        ldq, width, qp = _rows(q, "q", dev, T, hd)
+        Hq = width // hd
+        ldqo, _, qop = (ldq, width, qp) if q_out is q else _rows(q_out, "q_out", dev, T, Hq * hd)
+    elif q_out is not None:
         raise ValueError("q and q_out go together")
     k_pages, v_pages, k_exp, v_exp = cache.pointers
-    _lib.check(_lib.load().dg_kv_append_e4m3(
-        kp, vp, ldkv, qp, ldq, qop, ldqo, Hq, rp or None, rope_len, rot, 1 if interleaved else 0,
-        k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, page_table.data_ptr(),
-        max_pages, tok_start.data_ptr(), cache_len.data_ptr(), max_new, B, T, Hkv, hd,
-        _raw_stream(stream, dev)))
+    status = _lib.load().dg_kv_append_e4m3(
+        kp, vp, ldkv, qp, ldq, qop, ldqo, Hq, rp, rope_len, rot, 1 if interleaved else 0, k_pages,
+        v_pages, k_exp, v_exp, cache.n_pages, cache.page, pt, max_pages, ts, cl, max_new, B, T,
+        Hkv, hd, _raw_stream(stream, dev))
+    if status:
+        _lib.check(status)
 
 
 def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_prefix, out, *,
@@ -419,16 +430,16 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
     rows' own keys; max_prefix a bound on every cache_len.  ws: a Workspace of the caller's for
     this stream or graph; without one the call takes its scratch from torch's allocator.
     """
-    B, max_pages, dev = _paged_batch(cache, page_table, tok_start, cache_len)
+    pt, ts, cl, B, max_pages, dev = _paged_batch(cache, page_table, tok_start, cache_len)
     T, Hkv, hd = q.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return out
-    ldq, qp = _rows(q, "q", dev, T, n_q_heads * hd)
-    ldo, op = _rows(out, "out", dev, T, n_q_heads * hd)
+    ldq, _, qp = _rows(q, "q", dev, T, n_q_heads * hd)
+    ldo, _, op = _rows(out, "out", dev, T, n_q_heads * hd)
     zp = None
     if lse is not None:
-        if lse.dtype != _FLOAT32 or lse.shape != (T, n_q_heads) or not lse.is_contiguous() or \
-                lse.get_device() != dev:
+        if lse.dtype is not _FLOAT32 or lse.shape != (T, n_q_heads) or \
+                not lse.is_contiguous() or lse.get_device() != dev:
             raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
         zp = lse.data_ptr()
     lib = _lib.load()
@@ -441,11 +452,12 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
             buf = torch.empty(need, dtype=torch.uint8, device=q.device)
         wp, wn = buf.data_ptr(), need
     k_pages, v_pages, k_exp, v_exp = cache.pointers
-    _lib.check(lib.dg_paged_attn_e4m3(
-        qp, ldq, k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, page_table.data_ptr(),
-        max_pages, tok_start.data_ptr(), cache_len.data_ptr(), max_new, max_prefix, op, ldo, zp, B,
-        T, n_q_heads, Hkv, hd, hd ** -0.5 if scale is None else scale, mask, wp, wn,
-        _raw_stream(stream, dev)))
+    status = lib.dg_paged_attn_e4m3(
+        qp, ldq, k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, pt, max_pages, ts, cl,
+        max_new, max_prefix, op, ldo, zp, B, T, n_q_heads, Hkv, hd,
+        hd ** -0.5 if scale is None else scale, mask, wp, wn, _raw_stream(stream, dev))
+    if status:
+        _lib.check(status)
     return out
 
 
