@@ -701,17 +701,23 @@ struct PagedPlan {
   bool sorted;  // more CTAs than fit at once: the longest sequences first
 };
 
+// What a plan costs, in ns as measured: a CTA its set-up and epilogue and then
+// each key tile; a merge of splits its launch and, per split, the partial rows
+// written and read back (3.5 TB/s both ways).
+struct PagedCost {
+  double tile, fixed, merge, split;
+};
+
 // The split of `tiles` key tiles that ends soonest when `units` x splits CTAs
-// run `slots` at a time: a CTA costs its tiles and `fixed` tiles' time (its
-// set-up and epilogue: 14 us of 1.8 us a tile with many rows, 3 us of 0.8 us
-// with few), a merge of the splits `merge` once.
-int best_splits(long long units, int tiles, int slots, int fixed, int merge, int most) {
+// run `slots` at a time.
+int best_splits(long long units, int tiles, int slots, const PagedCost& c, int most) {
   int best = 1;
-  long long least = -1;
+  double least = 0;
   for (int s = 1; s <= std::min(tiles, most); ++s) {
     const long long waves = (units * s + slots - 1) / slots;
-    const long long cost = waves * (cdiv(tiles, s) + fixed) + (s > 1 ? merge : 0);
-    if (least < 0 || cost < least) {
+    const double cost = waves * (cdiv(tiles, s) * c.tile + c.fixed) +
+                        (s > 1 ? c.merge + s * c.split : 0.0);
+    if (s == 1 || cost < least) {
       least = cost;
       best = s;
     }
@@ -727,12 +733,13 @@ PagedPlan plan_paged(int B, int Hq, int Hkv, int hd, int max_new, long long max_
   const int tiles = (int)std::max(1ll, (max_keys + BKV - 1) / BKV);
   int splits, slots;
   long long units;
+  const double split_ns = (double)B * Hq * max_new * hd * sizeof(float) / 3500.0;
   if (rows <= 32) {
     pl.rows = rows <= 16 ? 16 : 32;
     pl.n_pairs = 1;
     units = (long long)B * Hkv;
     slots = kNumSMs * (pl.rows == 32 ? 1 : hd == 128 ? 2 : 3);
-    splits = best_splits(units, tiles, slots, 4, 4, kNumSMs * 2);
+    splits = best_splits(units, tiles, slots, {800.0, 3000.0, 3000.0, split_ns}, kNumSMs * 2);
     // Few units: as many splits as a cluster holds, merged by it (13.4 us, one
     // token over 4096 keys and 8 kv heads; 14.5 with a second launch), unless
     // they would be long or the clusters more than the GPU places at once.
@@ -747,7 +754,9 @@ PagedPlan plan_paged(int B, int Hq, int Hkv, int hd, int max_new, long long max_
     slots = kNumSMs;
     // a causal launch's row blocks see half the new keys on average, and its
     // grid has the long ones first: with enough of them it needs no split
-    splits = causal && units >= slots ? 1 : best_splits(units, tiles, slots, 7, 4, kNumSMs);
+    splits = causal && units >= slots
+                 ? 1
+                 : best_splits(units, tiles, slots, {1850.0, 8000.0, 2500.0, split_ns}, kNumSMs);
     splits = std::max(splits, cdiv(tiles, MAX_TILES));
   }
   pl.tiles_per_split = cdiv(tiles, splits);
