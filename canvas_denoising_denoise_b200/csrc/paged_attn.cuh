@@ -153,6 +153,35 @@ __device__ __forceinline__ int token_of(const AttnParams& p, int row) {
                           p.group_shift);
 }
 
+// Walks packed rows in equal steps: token, head of the group, and the element
+// offset token * ld + head * HD that they stand for (a division only at the start).
+template <int HD>
+struct RowWalk {
+  int tok, head;
+  int64_t at;
+  int step_tok, step_head;
+  int64_t step, wrap;
+  __device__ __forceinline__ RowWalk(const AttnParams& p, int row, int by, int ld) {
+    tok = token_of(p, row);
+    head = row - tok * p.group;
+    at = static_cast<int64_t>(tok) * ld + head * HD;
+    step_tok = token_of(p, by);
+    step_head = by - step_tok * p.group;
+    step = static_cast<int64_t>(step_tok) * ld + step_head * HD;
+    wrap = static_cast<int64_t>(ld) - p.group * HD;
+  }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    tok += step_tok;
+    head += step_head;
+    at += step;
+    if (head >= p.group) {
+      head -= p.group;
+      ++tok;
+      at += wrap;
+    }
+  }
+};
+
 // The smallest e with amax <= 448 2^e = 1.75 2^(e + 8), at least -100, from
 // the bf16 bits of a finite amax.
 __device__ __forceinline__ int q_exponent(uint32_t top) {
@@ -257,25 +286,14 @@ __device__ __forceinline__ void load_q_tile(const AttnParams& p, const Seq& s, i
   constexpr int PER = 32 / LANES;
   const int lane = lane_id();
   const int c8 = lane % LANES;
-  const __nv_bfloat16* base = p.q + static_cast<size_t>(s.t0) * p.ldq +
-                              static_cast<size_t>(g) * p.group * HD + c8 * 8;
-  // each step's loads come before its stores: the compiler keeps their order,
-  // and a chain of one row's latency after another's is what this costs
-  constexpr int BATCH = 8;
-#pragma unroll 1
-  for (int u = 0; u < 32 / PER; u += BATCH) {
-    const __nv_bfloat16* src[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int pr = min(first + r0 + (u + i) * PER + lane / LANES, rows - 1);
-      const int tok = token_of(p, pr);
-      src[i] = base + static_cast<int64_t>(tok) * p.ldq + (pr - tok * p.group) * HD;
-    }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int r = r0 + (u + i) * PER + lane / LANES;
-      copy16_async(raw + r * (2 * HD) + ((c8 ^ (r & 7)) << 4), src[i], first + r < rows);
-    }
+  const __nv_bfloat16* base = p.q + static_cast<int64_t>(s.t0) * p.ldq +
+                              static_cast<int64_t>(g) * p.group * HD + c8 * 8;
+  RowWalk<HD> walk(p, first + r0 + lane / LANES, PER, p.ldq);
+#pragma unroll 4
+  for (int u = 0; u < 32 / PER; ++u) {
+    const int r = r0 + u * PER + lane / LANES;
+    copy16_async(raw + r * (2 * HD) + ((c8 ^ (r & 7)) << 4), base + walk.at, first + r < rows);
+    walk.next(p);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
@@ -858,7 +876,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       constexpr int CPR = HD / 4;
       constexpr int RPW = 32 / CPR;  // rows per pass (1 or 2)
       const int cc = lane % CPR;
-      constexpr int BATCH = 8;  // loads ahead of the stores, as above
+      constexpr int BATCH = 8;  // loads ahead of the stores: the compiler keeps their order
+      const int pr0 = first + X * BQ + quarter * 32 + lane / CPR;
+      // partial rows [split][token][head][HD] or results [token][ldo]
+      const bool direct = p.n_splits == 1;
+      RowWalk<HD> walk(p, pr0, RPW, direct ? p.ldo : p.Hq * HD);
+      const int64_t base = static_cast<int64_t>(g) * p.group * HD + cc * 4;
+      __nv_bfloat16* out = p.out + static_cast<int64_t>(s.t0) * p.ldo + base;
+      float* part = p.part_o +
+                    (static_cast<int64_t>(split) * bt.T + s.t0) * p.Hq * HD + base;
 #pragma unroll 1
       for (int k0 = 0; k0 < 32; k0 += BATCH * RPW) {
         float4 v[BATCH];
@@ -869,20 +895,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-          const int pr = first + X * BQ + quarter * 32 + k0 + i * RPW + lane / CPR;
-          const int tok = token_of(p, pr);
-          const int h = g * p.group + pr - tok * p.group;
-          if (pr < rows) {
-            if (p.n_splits == 1) {
-              *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD +
-                                        cc * 4) =
+          if (pr0 + k0 + i * RPW < rows) {
+            if (direct)
+              *reinterpret_cast<uint2*>(out + walk.at) =
                   make_uint2(pack_bf16x2(v[i].x, v[i].y), pack_bf16x2(v[i].z, v[i].w));
-            } else {
-              const int64_t row =
-                  (static_cast<int64_t>(split) * bt.T + s.t0 + tok) * p.Hq + h;
-              reinterpret_cast<float4*>(p.part_o + row * HD)[cc] = v[i];
-            }
+            else
+              *reinterpret_cast<float4*>(part + walk.at) = v[i];
           }
+          walk.next(p);
         }
       }
     }
