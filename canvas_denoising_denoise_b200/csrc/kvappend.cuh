@@ -20,7 +20,7 @@
 // before its codes are formed): a thread owns the two 8-element chunks that
 // rotate with each other, so a rotation needs no exchange.  Queries are
 // rotated by further CTAs of the same launch; a thread keeps one row's angles
-// for several heads.
+// for several heads.  Rows are read once, past the caches' usual order.
 //
 // Bound by HBM for long prompts: four of up to 4096 rows (8 kv and 16 query
 // heads of 128) in 35 us, 4.4 TB/s, 66% of the measured copy rate, with a third
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(APPEND_THREADS, 3) append_kernel(const AppendP
 #pragma unroll
     for (int u = 0; u < Q_HEADS; ++u) {
       if (u < heads) {
-        ra[u] = *reinterpret_cast<const uint4*>(src + u * HD + ca * 8);
-        rb[u] = *reinterpret_cast<const uint4*>(src + u * HD + cb * 8);
+        ra[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * HD + ca * 8));
+        rb[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * HD + cb * 8));
       }
     }
     if (turn) {
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(APPEND_THREADS, 3) append_kernel(const AppendP
     ra[u] = rb[u] = make_uint4(0u, 0u, 0u, 0u);
     if (live && r >= r_beg && r < r_end) {
       const __nv_bfloat16* at = src + static_cast<int64_t>(r) * p.ldkv;
-      ra[u] = *reinterpret_cast<const uint4*>(at + ca * 8);
-      rb[u] = *reinterpret_cast<const uint4*>(at + cb * 8);
+      ra[u] = __ldcs(reinterpret_cast<const uint4*>(at + ca * 8));
+      rb[u] = __ldcs(reinterpret_cast<const uint4*>(at + cb * 8));
     }
   }
   float a[ROWS][8], c[ROWS][8];
