@@ -443,19 +443,32 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
             raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
         zp = lse.data_ptr()
     lib = _lib.load()
-    need = lib.dg_paged_attn_workspace_bytes(B, T, n_q_heads, Hkv, hd, max_new, max_prefix)
-    wp, wn = None, 0
-    if need and ws is not None:
-        wp, wn = ws.args(need)
-    elif need:
-        with torch.cuda.stream(stream):  # a no-op for None
-            buf = torch.empty(need, dtype=torch.uint8, device=q.device)
-        wp, wn = buf.data_ptr(), need
     k_pages, v_pages, k_exp, v_exp = cache.pointers
-    status = lib.dg_paged_attn_e4m3(
-        qp, ldq, k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, pt, max_pages, ts, cl,
-        max_new, max_prefix, op, ldo, zp, B, T, n_q_heads, Hkv, hd,
-        hd ** -0.5 if scale is None else scale, mask, wp, wn, _raw_stream(stream, dev))
+    if scale is None:
+        scale = hd ** -0.5
+
+    def call(wp, wn):
+        return lib.dg_paged_attn_e4m3(
+            qp, ldq, k_pages, v_pages, k_exp, v_exp, cache.n_pages, cache.page, pt, max_pages, ts,
+            cl, max_new, max_prefix, op, ldo, zp, B, T, n_q_heads, Hkv, hd, scale, mask, wp, wn,
+            _raw_stream(stream, dev))
+
+    def need():
+        return lib.dg_paged_attn_workspace_bytes(B, T, n_q_heads, Hkv, hd, max_new, max_prefix)
+
+    if ws is not None:
+        # a workspace that has grown to the shape once needs no query
+        buf = ws.buf
+        status = call(buf.data_ptr(), buf.numel()) if buf is not None else call(None, 0)
+        if status == _lib.DG_ERR_WORKSPACE_TOO_SMALL:
+            status = call(*ws.args(need()))
+    else:
+        wn, wp = need(), None
+        if wn:
+            with torch.cuda.stream(stream):  # a no-op for None
+                buf = torch.empty(wn, dtype=torch.uint8, device=q.device)
+            wp = buf.data_ptr()
+        status = call(wp, wn)
     if status:
         _lib.check(status)
     return out

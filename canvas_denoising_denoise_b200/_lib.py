@@ -15,6 +15,7 @@ c_char_p = ctypes.c_char_p
 P = ctypes.POINTER
 
 DG_OK = 0
+DG_ERR_WORKSPACE_TOO_SMALL = 4
 STATUS = {0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED_SHAPE",
           3: "DG_ERR_ALIGNMENT", 4: "DG_ERR_WORKSPACE_TOO_SMALL", 5: "DG_ERR_CUDA",
           6: "DG_ERR_TIMEOUT", 7: "DG_ERR_DEVICE_CHECK"}

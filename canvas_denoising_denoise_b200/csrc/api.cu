@@ -709,12 +709,13 @@ struct PagedCost {
 };
 
 // The split of `tiles` key tiles that ends soonest when `units` x splits CTAs
-// run `slots` at a time.
+// run `slots` at a time (more than four waves of them never pay).
 int best_splits(long long units, int tiles, int slots, const PagedCost& c, int most) {
   int best = 1;
   double least = 0;
   for (int s = 1; s <= std::min(tiles, most); ++s) {
     const long long waves = (units * s + slots - 1) / slots;
+    if (s > 1 && waves > 4) break;
     const double cost = waves * (cdiv(tiles, s) * c.tile + c.fixed) +
                         (s > 1 ? c.merge + s * c.split : 0.0);
     if (s == 1 || cost < least) {
