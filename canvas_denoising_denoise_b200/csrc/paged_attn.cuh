@@ -371,10 +371,10 @@ __device__ __forceinline__ int nth_longest(const Batch& bt, int want, int* scrat
 // other tile's work covers.  A softmax thread holds its 128 scores in
 // registers (read once), and hands P over in two halves of 64 keys, so that P V
 // starts while the second half is still being formed.
-// Measured: 32 heads x 256 rows over 32768 + 256 keys (hd 128) in 152 us with
-// the merge, 0.91 PFLOP/s, 57% of the measured bf16 rate; a 4096-row causal
-// prompt in 121 us, 53%.  Where the key range is short the set-up and the
-// epilogue of a CTA (14 us) weigh as much as its tiles.
+// Measured: 32 heads x 256 rows over 32768 + 256 keys (hd 128) in 150 us with
+// the merge, 0.92 PFLOP/s, 57% of the measured bf16 rate; a 4096-row causal
+// prompt behind 1031 rows in 120 us, 54%.  Where the key range is short the
+// set-up and epilogue of a CTA (8 us) weigh as much as its tiles.
 constexpr int WIDE_THREADS = 512;
 constexpr float P_SHIFT = 7.f;  // probabilities are held as 2^(s - m + 7): at most 2^15 in f16
 constexpr int V_SHIFT = 7;      // V codes as code 2^(ev - emax + 7): at most 57344 in f16
@@ -934,9 +934,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // The running maximum m is common to all keys of the CTA; the first tile sets
 // it, and it is only raised when a score would pass 2^8.5 (p carries 2^4): the
 // test costs one barrier with an OR a tile, the raise itself is rare.
-// Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 179 us, 6.0 TB/s,
-// 92% of the measured copy rate; of 20 to 100% of that length 116 us, 85%; one
-// sequence of 4097 keys 12 us, which is launch, first loads and the merge.  With
+// Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 165 us, 6.5 TB/s,
+// the measured copy rate; of 20 to 100% of that length 107 us, 92%; one
+// sequence of 4097 keys 9 us, which is launch, first loads and the merge.  With
 // hd 64 a tile has half the bytes and takes nearly as long (TMA moves as many
 // rows): 126 us where the bytes need 49.
 //
