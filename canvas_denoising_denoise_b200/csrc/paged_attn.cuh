@@ -937,8 +937,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 165 us, 6.5 TB/s,
 // the measured copy rate; of 20 to 100% of that length 107 us, 92%; one
 // sequence of 4097 keys 9 us, which is launch, first loads and the merge.  With
-// hd 64 a tile has half the bytes and takes nearly as long (TMA moves as many
-// rows): 126 us where the bytes need 49.
+// hd 64 a tile has half the bytes and takes as long (its chain of scores,
+// barrier, P and P V is the same): 150 us for the 64 of 8193 where the bytes
+// need 82.
 //
 // Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer, 2..5 = softmax (thread
 // = key; at the end thread = element of the head).
