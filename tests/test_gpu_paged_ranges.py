@@ -1,0 +1,105 @@
+"""dg_kv_append_e4m3 and dg_paged_attn_e4m3 at the ends of their ranges, against the oracle in 64 bits.
+
+Scores far below zero, rows of zeros, weights far below the largest, page scales
+of every size.  Where nothing else is said the bounds are those of
+test_gpu_paged.compare.
+"""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_paged as base
+from oracle import paged
+from paged_cases import Case
+from test_gpu_paged import dg
+
+pytestmark = pytest.mark.gpu
+
+_compare = base.compare
+
+
+def compare(case, out, z, *args, **kw):
+    """base.compare, which takes the largest error with max() and so passes over NaN, for results
+    that have to be finite."""
+    assert torch.isfinite(out.float()).all(), "results that are not finite"
+    assert z is None or torch.isfinite(z).all(), "log-sum-exps that are not finite"
+    _compare(case, out, z, *args, **kw)
+
+
+def check_attention(*args, **kw):
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(base, "compare", compare)
+        return base.check_attention(*args, **kw)
+
+
+def test_the_other_files_results_are_finite(monkeypatch):
+    """The batches of test_gpu_paged once more (their rows see finite keys and values only)."""
+    monkeypatch.setattr(base, "compare", compare)
+    for causal in (False, True):
+        for hd, page in ((64, 16), (128, 128), (64, 64), (128, 32)):
+            base.test_attention_many_rows(hd, page, causal)
+            base.test_attention_few_rows(hd, page, causal)
+    for hkv, group, n in ((1, 7, 40), (2, 16, 1), (1, 32, 2), (1, 20, 3), (8, 2, 1), (2, 25, 1)):
+        base.test_attention_groups(hkv, group, n)
+    base.test_attention_long_key_ranges()
+    base.test_attention_scales_differ_between_pages()
+    base.test_attention_peaked_rows_and_small_weights()
+    base.test_attention_options()
+    base.test_append_then_attend_as_a_program_does()
+    base.test_attention_of_more_sequences_than_fit_at_once(48, 8, 2, 1)
+    base.test_append_and_attention_on_two_streams_at_once()
+
+
+# Ways that the few-row kernel is launched: (lengths, kv heads, group).  One key;
+# several tiles by one CTA; a range per CTA of a cluster; ranges that a second
+# launch merges; and the 32-row form unsplit and split.
+NARROW = {
+    "one key": ([(1, 0)], 2, 2),
+    "one CTA": ([(1, 300)] * 40, 8, 1),
+    "cluster": ([(1, 1000)], 1, 2),
+    "merge launch": ([(1, 3000), (1, 2000), (1, 900)], 8, 2),
+    "32 rows": ([(1, 700), (1, 90)], 1, 20),
+    "32 rows, merge launch": ([(3, 2000)] * 20, 1, 8),
+}
+WIDE = {"wide": ([(150, 300)], 2, 2), "wide, split": ([(150, 3000)], 1, 1)}
+
+
+def lowered(kind, nats, keys=None, hd=64, seed=80):
+    """A batch whose scores lie `nats` lower (at the positions `keys` only, where given): element 0
+    of every query times element 0 of every key."""
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    case = Case(lengths, hkv, group, hd, 64, seed=seed, exp_range=(121, 122))
+    case.q[:, ::hd] = -nats * hd ** 0.5 / 7.0  # against the keys' 448 * 2^(121 - 127) = 7
+    for _, n, c, pages in case.seqs:
+        live = np.arange(len(pages) * 64).reshape(-1, 64)
+        at = live < n + c if keys is None else keys(live, n + c)
+        column = case.cache["k"][pages][..., 0]
+        column[:] = np.where((live < n + c)[:, None], 0, column)
+        column[np.broadcast_to(at[:, None], column.shape) &
+               np.broadcast_to((live < n + c)[:, None], column.shape)] = 0x7E
+        block = case.cache["k"][pages]
+        block[..., 0] = column
+        case.cache["k"][pages] = block
+    return case
+
+
+@pytest.mark.parametrize("nats", [64.0, 100.0, 300.0])
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
+def test_scores_far_below_zero(kind, nats):
+    check_attention(lowered(kind, nats), True)
+
+
+@pytest.mark.parametrize("kind", ["one CTA", "cluster", "merge launch", "32 rows, merge launch", "wide, split"])
+@pytest.mark.parametrize("far", ["first", "last"])
+def test_some_key_ranges_far_below_the_others(kind, far):
+    keys = (lambda p, total: p < total // 2) if far == "first" else (lambda p, total: p >= total // 2)
+    check_attention(lowered(kind, 200.0, keys), True)
+
+
+@pytest.mark.parametrize("kind", ["one key", "one CTA", "cluster"])
+def test_scores_below_zero_under_pages_of_zero_values(kind):
+    case = lowered(kind, 80.0)
+    case.cache["v"][:] = 0
+    case.cache["v_exp"][:] = 127 - 40  # as append stores zeros
+    out = check_attention(case, True)
+    assert (out == 0).all()
