@@ -1283,9 +1283,9 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
             const float d = fmaxf(fmaxf(sRed[r], sRed[NR + r]),
                                   fmaxf(sRed[2 * NR + r], sRed[3 * NR + r])) - N_SHIFT;
             const float up = d == -INFINITY ? 0.f : (j > 0 ? fmaxf(d, 0.f) : d);
-            // nothing has been summed before the first tile, whose up may be so
-            // far below zero that 2^-up is infinite
-            fac[e] = j > 0 ? attn::fast_exp2(-up) : 1.f;
+            // (the first tile, with nothing summed before it, has an up of any
+            // sign: 2^-up may be infinite, and times the empty sums NaN)
+            fac[e] = attn::fast_exp2(-fmaxf(up, 0.f));
             l[r] *= fac[e];
             x[r] -= up;
             if (r == kl) mine = m_now[r] + up;
