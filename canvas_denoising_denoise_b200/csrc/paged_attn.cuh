@@ -922,18 +922,22 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // and one softmax thread would walk all 128 keys of a tile alone.  So the
 // products are transposed: per tile of 128 keys
 //     S^T [keys x 2 NR]  = K [hi | lo]^T      A = K tile, B = query halves
-//     O^T [hd x 4 NR]   += V^T [p0 p1 p2 0]   A = V tile (M-major), B = P
+//     O^T [hd x 4 NR]   += V^T [p0 p1 p2 p3]  A = V tile (M-major), B = P
 // NR (16 or 32) holds the rows.  A thread owns one key: its page's scales are
-// per-thread constants and its NR probabilities are 3 x NR bytes, one 16-byte
-// store per 16.  A probability p (times the page's V scale) enters as three
-// e4m3 terms p0 + p1/16 + p2/256, each the rounding of what the terms before
-// left: 11 bits of it, down to 2^-22 of the largest.  Both products read the
+// per-thread constants and its NR probabilities are 4 x NR bytes, one 16-byte
+// store per 16.  A probability p (times the page's V scale) is rounded to f16
+// and enters as four e4m3 terms p0 + p1/32 + p2/32^2 + p3/32^3, each the
+// rounding of what the terms before left.  Up to p = 2^8 a term's remainder
+// times 32 stays within e4m3's range, and the four hold every f16 value
+// exactly (the last one's smallest step is f16's, 2^-24): weights keep 2^-11
+// of themselves down to 2^-18 of the largest and 2^-29 of that below, so that
+// many small ones beside a large one are not lost.  Both products read the
 // codes as TMA delivered them: the kernel streams the cache and does nothing
 // else to it, and is bound by HBM once there are enough keys.
 //
 // The running maximum m is common to all keys of the CTA; the first tile sets
-// it, and it is only raised when a score would pass 2^8.5 (p carries 2^4): the
-// test costs one barrier with an OR a tile, the raise itself is rare.
+// it, and it is only raised when a p would pass 2^8 (the largest starts at 2^4):
+// the test costs one barrier with an OR a tile, the raise itself is rare.
 // Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 165 us, 6.5 TB/s,
 // the measured copy rate; of 20 to 100% of that length 107 us, 92%; one
 // sequence of 4097 keys 9 us, which is launch, first loads and the merge.  With
@@ -945,7 +949,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // = key; at the end thread = element of the head).
 constexpr int NARROW_THREADS = 192;
 constexpr float N_SHIFT = 4.f;
-constexpr float N_LIMIT = 8.5f;  // 2^8.5 = 362 <= 448
+constexpr float N_LIMIT = 8.f;
+constexpr int P_TERMS = 4;       // e4m3 terms of a probability
+constexpr float P_STEP = 32.f;   // between them
 
 template <int HD, int NR>
 struct Narrow {
@@ -1002,7 +1008,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;                        // ST tiles
   uint8_t* sV = sK + ST * CF::T_BYTES;       // ST tiles (a head of 64 reads 512 bytes past one)
-  uint8_t* sP = sV + ST * CF::T_BYTES;       // [128 keys][p0 | p1 | p2 | 0]
+  uint8_t* sP = sV + ST * CF::T_BYTES;       // [128 keys][p0 | p1 | p2 | p3]
   uint8_t* sQ = sP + CF::P_BYTES;            // [NR hi rows][NR lo rows]
   float* sF = reinterpret_cast<float*>(sQ + CF::Q_BYTES);  // [NR] row factors
   float* sM = sF + NR;                                     // [2][NR] running maxima (log2 units)
@@ -1168,11 +1174,6 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
-    // the unused fourth of every P row
-#pragma unroll
-    for (int c = 0; c < NR / 16; ++c)
-      *reinterpret_cast<uint4*>(sP + p_swz<NR>(kl, 3 * (NR / 16) + c)) =
-          make_uint4(0u, 0u, 0u, 0u);
     // page scales of this thread's key, one tile ahead
     auto page_id = [&](int j) -> int {
       const int at = ((t_beg + j) << log_ppt) + (kl >> bt.log_page);
@@ -1292,7 +1293,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
           }
           if (j > 0) {
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
+            for (int term = 0; term < P_TERMS; ++term) {
               uint32_t o[16];
               tmem_ld16(tl + 4 * NR + term * NR + c, o);
               tmem_ld_wait();
@@ -1313,11 +1314,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (j - 1) & 1, abort_flag, 0x583));
 #pragma unroll
       for (int c = 0; c < NR; c += 16) {
-        uint32_t w[3][4] = {};
+        uint32_t w[P_TERMS][4] = {};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (CF::stops(c + 4 * q, rows)) break;
-          uint32_t term[3][2];
+          uint32_t term[P_TERMS][2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = c + 4 * q + 2 * e;
@@ -1326,20 +1327,20 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
             l[r + 1] = fmaf(p1, l_scale, l[r + 1]);
             __half2 rest = __floats2half2_rn(p0, p1);
 #pragma unroll
-            for (int t = 0; t < 3; ++t) {
+            for (int t = 0; t < P_TERMS; ++t) {
               const __nv_fp8x2_storage_t code =
                   __nv_cvt_halfraw2_to_fp8x2(__half2_raw(rest), __NV_SATFINITE, __NV_E4M3);
               term[t][e] = code;
-              if (t < 2)
+              if (t < P_TERMS - 1)
                 rest = __hmul2(__hsub2(rest, __half2(__nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3))),
-                               __float2half2_rn(16.f));
+                               __float2half2_rn(P_STEP));
             }
           }
 #pragma unroll
-          for (int t = 0; t < 3; ++t) w[t][q] = term[t][0] | (term[t][1] << 16);
+          for (int t = 0; t < P_TERMS; ++t) w[t][q] = term[t][0] | (term[t][1] << 16);
         }
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
+        for (int t = 0; t < P_TERMS; ++t)
           *reinterpret_cast<uint4*>(sP + p_swz<NR>(kl, t * (NR / 16) + c / 16)) =
               make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
       }
@@ -1407,18 +1408,19 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
 #pragma unroll
     for (int c = 0; c < NR; c += 16) {
       if (c >= rows) break;
-      uint32_t o0[16], o1[16], o2[16];
-      tmem_ld16(tl + 4 * NR + c, o0);
-      tmem_ld16(tl + 5 * NR + c, o1);
-      tmem_ld16(tl + 6 * NR + c, o2);
+      uint32_t o[P_TERMS][16];
+#pragma unroll
+      for (int t = 0; t < P_TERMS; ++t) tmem_ld16(tl + (4 + t) * NR + c, o[t]);
       tmem_ld_wait();
       if (kl < HD) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int r = c + e;
           if (r >= rows) break;
-          const float v = fmaf(__uint_as_float(o2[e]), 1.f / 256.f,
-                               fmaf(__uint_as_float(o1[e]), 1.f / 16.f, __uint_as_float(o0[e])));
+          float v = __uint_as_float(o[P_TERMS - 1][e]);
+#pragma unroll
+          for (int t = P_TERMS - 2; t >= 0; --t)
+            v = fmaf(v, 1.f / P_STEP, __uint_as_float(o[t][e]));
           const int h = g * p.group + hh;
           if (p.merge)
             sO[r * HD + kl] = v;

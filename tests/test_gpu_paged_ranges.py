@@ -103,3 +103,60 @@ def test_scores_below_zero_under_pages_of_zero_values(kind):
     case.cache["v_exp"][:] = 127 - 40  # as append stores zeros
     out = check_attention(case, True)
     assert (out == 0).all()
+
+
+def check_sink(kind, bits, quantum, page=64):
+    """Key 0 stands `bits` (log2) above every other key and its value is zero: the result is made of
+    the small weights alone.  A weight w_j is held to 2^-11 of itself (f16), and to `quantum` of the
+    largest; exp2, the fp32 sums and the result's rounding add 2^-12 and 2^-8 relative:
+        |error| <= (2^-8 + 2^-10) |out| + quantum w_0 sum_j |v_j|.
+    """
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    case = Case(lengths, hkv, group, 64, page, seed=81, exp_range=(121, 122))
+    case.q[:] = 0.0
+    case.q[:, ::64] = 4.0
+    case.cache["v"] &= 0x7F  # all positive (the NaN codes behind the sequences stay)
+    for _, n, c, pages in case.seqs:
+        case.cache["k"][pages[0], :, 0] = 0
+        block = case.cache["k"][pages]
+        block[..., 0] = np.where(block[..., 0] == 0x7F, 0x7F, 0)
+        case.cache["k"][pages] = block
+        case.cache["k"][pages[0], :, 0, 0] = 0x7E  # 448 * 2^-6 = 7, times 4
+        case.cache["v"][pages[0], :, 0] = 0
+    d = dg()
+    cache, table, starts, lens = case.device()
+    out = torch.zeros((case.T, case.hq * 64), dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros((case.T, case.hq), device="cuda")
+    scale = bits / (28.0 * np.log2(np.e))
+    d.paged_attn_e4m3(case.q.cuda(), cache, table, starts, lens, case.max_new, case.max_prefix, out,
+                      n_q_heads=case.hq, lse=z, scale=scale, mask=d.MASK_CAUSAL)
+    torch.cuda.synchronize()
+    d.check_device_errors()
+    q = case.heads("q").astype(np.float64)
+    want, wz = paged.attend(case.cache, case.seqs, q, True, scale)
+    got = out.float().cpu().numpy().astype(np.float64).reshape(want.shape)
+    assert np.isfinite(got).all()
+    worst = 0.0
+    for t0, n, c, pages in case.seqs:
+        for g in range(hkv):
+            v = paged.keys_of(case.cache, "v", pages, g, c + n)
+            hs = slice(g * group, (g + 1) * group)
+            w = want[t0:t0 + n, hs]
+            tol = (2.0 ** -8 + 2.0 ** -10) * w + quantum * np.abs(v).sum(0)
+            worst = max(worst, float((np.abs(got[t0:t0 + n, hs] - w) / tol).max()))
+    assert worst <= 1.0, worst
+    assert np.abs(z.cpu().numpy() - wz).max() <= 2.0 ** -19 * (1 + np.abs(wz).max())
+
+
+# the largest weight is held as 2^4 or more, and f16's half step below 2^-14 is 2^-25
+@pytest.mark.parametrize("bits", [12.6, 20.3, 24.6])
+@pytest.mark.parametrize("kind", [k for k in NARROW if k != "one key"])
+def test_small_weights_beside_a_sink_few_rows(kind, bits):
+    check_sink(kind, bits, 2.0 ** -29)
+
+
+# the largest weight is held as 2^7 or more
+@pytest.mark.parametrize("bits", [12.6, 20.3, 27.4])
+@pytest.mark.parametrize("kind", [*WIDE])
+def test_small_weights_beside_a_sink_many_rows(kind, bits):
+    check_sink(kind, bits, 2.0 ** -32)
