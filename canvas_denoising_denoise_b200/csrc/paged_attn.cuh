@@ -938,6 +938,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // The running maximum m is common to all keys of the CTA; the first tile sets
 // it, and it is only raised when a p would pass 2^8 (the largest starts at 2^4):
 // the test costs one barrier with an OR a tile, the raise itself is rare.
+//
+// Value scales.  With e the exponent of the key's page and E a reference common
+// to the CTA, p = 2^(s - m + e - E + 4) goes into the product and p 2^(E - e)
+// into the sum.  E is the first tile's largest e and follows one that lies more
+// than 2^30 above it (in a raise); an e below E - 48 counts as E - 48, and its
+// values, too small to matter, as zero.  So p 2^(E - e) stays between 2^-30 and
+// 2^56 for the largest weight, whatever the scales, and no weight above 2^-50
+// of the largest is lost from the sum.
 // Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 165 us, 6.5 TB/s,
 // the measured copy rate; of 20 to 100% of that length 107 us, 92%; one
 // sequence of 4097 keys 9 us, which is launch, first loads and the merge.  With
@@ -950,6 +958,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 constexpr int NARROW_THREADS = 192;
 constexpr float N_SHIFT = 4.f;
 constexpr float N_LIMIT = 8.f;
+constexpr int V_SPREAD = 48;     // value scales further below the reference are left out
+constexpr int V_LAG = 30;        // how far a value scale may lie above it
 constexpr int P_TERMS = 4;       // e4m3 terms of a probability
 constexpr float P_STEP = 32.f;   // between them
 
@@ -963,6 +973,7 @@ struct Narrow {
   static constexpr int TMEM = 8 * NR;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * 2 * T_BYTES + P_BYTES + Q_BYTES + NR * 4 * 8 + 256;
+  static_assert((1 + 4 * STAGES + 5) * 8 + 3 * 4 + 4 * 4 <= 256, "barriers, flags and exponents");
   static constexpr uint32_t IDESC_S = idesc_e4m3_f32(BKV, 2 * NR);
   // A and B both M/N-major; the M = 128 lanes beyond a head of 64 are unused
   static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(128, 4 * NR) | (1u << 15) | (1u << 16);
@@ -1027,6 +1038,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* s_fail = abort_flag + 1;  // a softmax thread gave up waiting
+  int* sE = reinterpret_cast<int*>(tmem_holder + 3);  // [4] largest value exponents of the warps
 
   const int warp = warp_id();
   const int lane = lane_id();
@@ -1170,17 +1182,14 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     const int quarter = warp & 3;
     const int kl = quarter * 32 + lane;  // key of the tile; later element of the head
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    load_q_rows<HD, NR / 4>(p, s, g, 0, rows, sQ, sQ + NR * HD, sF, (warp - 2) * (NR / 4));
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(q_full);
     // page scales of this thread's key, one tile ahead
     auto page_id = [&](int j) -> int {
       const int at = ((t_beg + j) << log_ppt) + (kl >> bt.log_page);
       return j < n && at < pages ? table[at] : -1;
     };
     auto page_exps = [&](int pg, int* ke, int* ve) {
-      *ke = *ve = 127;
+      *ke = 127;
+      *ve = 0;  // no page: below every reference
       if (pg >= 0 && pg < bt.n_pages) {
         const size_t at = static_cast<size_t>(pg) * p.Hkv + g;
         *ke = p.k_exp[at];
@@ -1194,21 +1203,33 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     };
     int ke, ve;
     int pg = page_id(0);
+    load_q_rows<HD, NR / 4>(p, s, g, 0, rows, sQ, sQ + NR * HD, sF, (warp - 2) * (NR / 4));
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
     page_exps(pg, &ke, &ve);
     check_page(0, pg);
     pg = page_id(1);
+    auto warp_exponents = [&](int e) {
+      const int top = __reduce_max_sync(0xffffffffu, e);
+      if (lane == 0) sE[quarter] = top;
+    };
+    auto top_exponent = [&]() { return max(max(sE[0], sE[1]), max(sE[2], sE[3])); };
+    warp_exponents(ve);
     const int open_keys = p.causal ? s.c0 + 1 : total;  // keys below are visible to every row
     float l[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) l[r] = 0.f;
-    bar_any(1, 128, false);  // row factors are in place
+    bar_any(1, 128, false);  // row factors and exponents are in place
+    int e_ref = top_exponent();
     bool ok = true;
     int cur = 0;  // which of sM holds the maxima
     int j = 0;
     for (; j < n; ++j) {
       const float kf = __uint_as_float(static_cast<uint32_t>(ke) << 23);
-      const float ev = static_cast<float>(ve - 127);
-      const float l_scale = __uint_as_float(static_cast<uint32_t>(254 - ve) << 23);  // 2^-ev
+      const int ve_now = ve;
+      int eff = max(ve_now, e_ref - V_SPREAD);
+      const float shift = static_cast<float>(eff - e_ref) + N_SHIFT;
       if (j + 1 < n) {
         page_exps(pg, &ke, &ve);
         check_page(j + 1, pg);
@@ -1221,9 +1242,9 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
                       ok && mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag, 0x581));
       tc_fence_after();
       float x[NR];
-      // x = score in log2 units + ev (the V scale) + shift - running maximum
+      // x = score in log2 units + shift (the V scale) - running maximum
       const float* m_now = sM + cur * NR;
-      bool above = false;
+      bool above = ve_now > e_ref + V_LAG;
 #pragma unroll
       for (int c = 0; c < NR; c += 16) {
         uint32_t hi[16], lo[16];
@@ -1239,7 +1260,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float sum = __uint_as_float(hi[q + e]) + __uint_as_float(lo[q + e]);
-            x[c + q + e] = fmaf(sum, ff[e] * kf, (ev + N_SHIFT) - mm[e]);
+            x[c + q + e] = fmaf(sum, ff[e] * kf, shift - mm[e]);
             if (edge && pos >= sSees[c + q + e]) x[c + q + e] = -INFINITY;
             above = above || x[c + q + e] > N_LIMIT;
           }
@@ -1253,6 +1274,21 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         *s_fail = 1;
       }
       if (raise) {
+        float shrink = 1.f;  // 2^ of how far the reference exponent falls behind
+        if (j > 0) {
+          warp_exponents(ve_now);
+          bar_any(1, 128, false);
+          const int top = top_exponent();
+          if (top > e_ref + V_LAG) {
+            const int was = eff;
+            eff = max(eff, top - V_SPREAD);
+            const float move = static_cast<float>(eff - was - (top - e_ref));
+            shrink = attn::fast_exp2(static_cast<float>(e_ref - top));
+#pragma unroll
+            for (int r = 0; r < NR; ++r) x[r] += move;
+            e_ref = top;
+          }
+        }
         // raise the maxima to this tile's
 #pragma unroll
         for (int r = 0; r < NR; r += 4) {
@@ -1299,7 +1335,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * fac[e]);
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * (fac[e] * shrink));
               tmem_st16(tl + 4 * NR + term * NR + c, o);
             }
           }
@@ -1309,6 +1345,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         cur ^= 1;
         bar_any(1, 128, false);
       }
+      const float l_scale = pow2(e_ref - eff);
       // P rows may be rewritten once the previous product has read them
       if (j > 0)
         ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (j - 1) & 1, abort_flag, 0x583));
@@ -1343,6 +1380,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         for (int t = 0; t < P_TERMS; ++t)
           *reinterpret_cast<uint4*>(sP + p_swz<NR>(kl, t * (NR / 16) + c / 16)) =
               make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+      }
+      if (ve_now < eff) {  // (the values count as zero, but the weights as weights)
+#pragma unroll
+        for (int c = 0; c < 4 * NR / 16; ++c)
+          *reinterpret_cast<uint4*>(sP + p_swz<NR>(kl, c)) = make_uint4(0u, 0u, 0u, 0u);
       }
       if (pos >= total) {
         // whatever lies behind the sequence's end must not meet the product
@@ -1391,8 +1433,10 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     if (kl < NR) {
       sum = (sRed[kl] + sRed[NR + kl]) + (sRed[2 * NR + kl] + sRed[3 * NR + kl]);
       if (!ok) sum = 0.f;
-      sF[kl] = p.merge ? sum : (sum == 0.f ? 0.f : 1.f / sum);
+      sRed[kl] = sum == 0.f ? 0.f : 1.f / sum;  // this thread alone reads it above
+      sF[kl] = sum;
     }
+    const float v_scale = pow2(e_ref - 127);
     if (kl < rows && !p.merge) {
       const int tok = token_of(p, kl);
       const int64_t at = static_cast<int64_t>(s.t0 + tok) * p.Hq + g * p.group + kl - tok * p.group;
@@ -1421,14 +1465,14 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
 #pragma unroll
           for (int t = P_TERMS - 2; t >= 0; --t)
             v = fmaf(v, 1.f / P_STEP, __uint_as_float(o[t][e]));
+          v = v * sRed[r] * v_scale;  // (their product might overflow)
           const int h = g * p.group + hh;
           if (p.merge)
             sO[r * HD + kl] = v;
           else if (p.n_splits > 1)
-            p.part_o[(part + static_cast<int64_t>(s.t0 + tok) * p.Hq + h) * HD + kl] = v * sF[r];
+            p.part_o[(part + static_cast<int64_t>(s.t0 + tok) * p.Hq + h) * HD + kl] = v;
           else
-            p.out[static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD + kl] =
-                __float2bfloat16_rn(v * sF[r]);
+            p.out[static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD + kl] = __float2bfloat16_rn(v);
           if (++hh == p.group) {
             hh = 0;
             ++tok;
@@ -1438,7 +1482,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
     }
   }
   if (p.merge) {
-    // Every split's O, sums (sF) and maxima (sM) lie in its CTA's shared
+    // Every split's results, sums (sF) and maxima (sM) lie in its CTA's shared
     // memory; the CTAs of the cluster share the rows x hd results.
     cluster_arrive_wait();
     if (threadIdx.x >= 64) {
@@ -1466,17 +1510,18 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
         float sum = 0.f, v = 0.f;
 #pragma unroll
         for (int k = 0; k < MAX_CLUSTER; ++k) {
-          // a split without a visible key left its O unwritten
-          if (f[k] != 0.f) {
-            const float e = attn::fast_exp2(m[k] - top);
-            sum = fmaf(e, f[k], sum);
-            v = fmaf(e, o[k], v);
-          }
+          // a split without a visible key weighs nothing, whatever it left
+          if (f[k] != 0.f) f[k] *= attn::fast_exp2(m[k] - top);
+          sum += f[k];
         }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k)
+          if (f[k] != 0.f) v = fmaf(f[k] * inv, o[k], v);
         const int tok = token_of(p, r);
         const int h = g * p.group + r - tok * p.group;
         p.out[static_cast<int64_t>(s.t0 + tok) * p.ldo + h * HD + (i & (HD - 1))] =
-            __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+            __float2bfloat16_rn(v);
         if (p.lse && (i & (HD - 1)) == 0)
           p.lse[static_cast<int64_t>(s.t0 + tok) * p.Hq + h] =
               sum == 0.f ? -INFINITY : (top - N_SHIFT + log2f(sum)) * 0.69314718055994531f;

@@ -349,10 +349,10 @@ int dg_kv_append_e4m3(const void* k, const void* v, int ldkv, const void* q, int
  *   split over keys; a larger length is reported like the errors above)
  * Queries enter the product at bf16 precision (a row's elements below 2^-10 of
  * its largest to 2^-18 of that), key and value codes as they are cached; a
- * probability (times its page's value scale) is rounded to 2^-11 of itself, or
- * to 2^-29 of the largest where that is more; sums and softmax statistics are fp32.
- * Values more than 2^31 below the largest page scale among a sequence's pages
- * may be lost.  Exponents must lie in [1, 254].  Positions from
+ * probability is rounded to 2^-11 of itself, and where that is more, it times
+ * its page's value scale to 2^-29 of the largest probability times the largest
+ * value scale of its sequence's pages; sums and softmax statistics are fp32.
+ * Exponents must lie in [1, 254], scaled scores within +-2^23.  Positions from
  * cache_len[b] + n_b on may hold any codes, NaN among them.  A NaN or an
  * infinity in a query row makes that row NaN; a NaN code at a cached position
  * makes NaN of the rows that see it, and may of earlier rows of its sequence.

@@ -89,6 +89,12 @@ def test_scores_far_below_zero(kind, nats):
     check_attention(lowered(kind, nats), True)
 
 
+@pytest.mark.parametrize("nats", [2.0 ** 22, -2.0 ** 22])
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
+def test_scores_of_millions_stay_finite(kind, nats):
+    check_attention(lowered(kind, nats), True)  # (the bounds grow with the scores)
+
+
 @pytest.mark.parametrize("kind", ["one CTA", "cluster", "merge launch", "32 rows, merge launch", "wide, split"])
 @pytest.mark.parametrize("far", ["first", "last"])
 def test_some_key_ranges_far_below_the_others(kind, far):
@@ -160,3 +166,99 @@ def test_small_weights_beside_a_sink_few_rows(kind, bits):
 @pytest.mark.parametrize("kind", [*WIDE])
 def test_small_weights_beside_a_sink_many_rows(kind, bits):
     check_sink(kind, bits, 2.0 ** -32)
+
+
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
+@pytest.mark.parametrize("exp", [30, 87, 200, 227, 253, 254])
+def test_value_scales_at_the_ends(kind, exp):
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    case = Case(lengths, hkv, group, 64, 32, seed=83, exp_range=(121, 122))
+    small_values(case)
+    case.cache["v_exp"][:] = exp
+    check_attention(case, True)
+
+
+@pytest.mark.parametrize("kind", [*NARROW])
+@pytest.mark.parametrize("exp", [1, 2])
+def test_value_scales_at_the_lower_end(kind, exp):
+    """Results of 2^-126 and less: bf16 values lie 2^-133 apart there, so that their rounding is off
+    by up to 2^-134 whatever the value, which compare()'s 2^-8 |out| does not hold.  With it:
+        |error| <= 2^-134 + 2^-8 |out| + (2^-10 + 2 ds) max|v|   (ds as in base.compare).
+    """
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    case = Case(lengths, hkv, group, 64, 32, seed=83, exp_range=(121, 122))
+    small_values(case)
+    case.cache["v_exp"][:] = exp
+    worst = []
+
+    def compare_small(case, out, z, causal, scale):
+        want, wz = paged.attend(case.cache, case.seqs, case.heads("q").astype(np.float64), causal, scale)
+        got = out.float().cpu().numpy().astype(np.float64).reshape(want.shape)
+        assert np.isfinite(got).all()
+        for t0, n, c0, pages in case.seqs:
+            for g in range(case.hkv):
+                k, v = (paged.keys_of(case.cache, x, pages, g, c0 + n) for x in "kv")
+                hs = slice(g * case.group, (g + 1) * case.group)
+                q = case.heads("q")[t0:t0 + n, hs].astype(np.float64)
+                ds = 2.0 ** -18 * np.abs(q).max(-1) * scale * np.abs(k).sum(1).max()
+                w = want[t0:t0 + n, hs]
+                tol = 2.0 ** -134 + 2.0 ** -8 * np.abs(w) + ((2.0 ** -10 + 2 * ds) * np.abs(v).max())[..., None]
+                worst.append((np.abs(got[t0:t0 + n, hs] - w) / tol).max())
+                worst.append((np.abs(z.cpu().numpy()[t0:t0 + n, hs] - wz[t0:t0 + n, hs]) /
+                              (ds + 2.0 ** -19 * (1 + np.abs(wz[t0:t0 + n, hs])))).max())
+
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(base, "compare", compare_small)
+        base.check_attention(case, True)
+    assert np.max(worst) <= 1.0, np.max(worst)
+
+
+def small_values(case):
+    """Value codes of magnitude 1 at most, so that 2^127 times them is finite; NaN ones stay."""
+    nan = (case.cache["v"] & 0x7F) == 0x7F
+    g = torch.Generator().manual_seed(84)
+    x = (torch.randn(case.cache["v"].shape, generator=g) * 0.3).clamp(-1, 1)
+    codes = x.to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    case.cache["v"] = np.where(nan, np.uint8(0x7F), codes)
+
+
+def spread_case(kind, exps, page=16):
+    """Page i of a sequence has the value exponent exps[i % len(exps)]."""
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    case = Case(lengths, hkv, group, 64, page, seed=85, exp_range=(121, 122))
+    small_values(case)
+    for _, _, _, pages in case.seqs:
+        case.cache["v_exp"][pages] = np.resize(exps, len(pages))[:, None]
+    return case
+
+
+@pytest.mark.parametrize("kind", [k for k in (*NARROW, *WIDE) if k != "one key"])
+@pytest.mark.parametrize("exps", [(227, 87), (87, 227), (1, 254), (87, 110, 130, 160, 180, 227),
+                                  tuple(range(254, 0, -9)), tuple(range(1, 255, 9))])
+def test_value_scales_far_apart_keep_the_weights(kind, exps):
+    check_attention(spread_case(kind, exps), True)
+
+
+@pytest.mark.parametrize("kind", [k for k in (*NARROW, *WIDE) if k != "one key"])
+def test_value_scales_far_apart_in_blocks_of_pages(kind):
+    # whole tiles of small scales before and behind whole tiles of large ones
+    check_attention(spread_case(kind, (87,) * 16 + (227,) * 16), True)
+    check_attention(spread_case(kind, (227,) * 16 + (87,) * 16), True)
+    check_attention(spread_case(kind, (100,) * 8 + (140,) * 8 + (180,) * 8 + (110,) * 8), True)
+
+
+@pytest.mark.parametrize("kind", [k for k in (*NARROW, *WIDE) if k != "one key"])
+@pytest.mark.parametrize("low", [0, 1])
+def test_large_weights_under_small_value_scales(kind, low):
+    """The keys of pages with the small scale stand 60 nats above the others (log-sum-exp tells)."""
+    case = spread_case(kind, (87, 227) if low == 0 else (227, 87))
+    case.q[:] = 0.0
+    case.q[:, ::64] = 4.0
+    for _, n, c, pages in case.seqs:
+        block = case.cache["k"][pages]
+        nan = block[..., 0] == 0x7F
+        block[..., 0] = 0
+        block[low::2, :, :, 0] = 0x7E
+        block[..., 0][nan] = 0x7F
+        case.cache["k"][pages] = block
+    check_attention(case, True, scale=60.0 / 28.0)
