@@ -1541,6 +1541,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 :
 // Merge of the key-range splits: out = sum_s w_s O_s / sum_s w_s with
 // w_s = 2^(lse_s - max).  A warp per (token, head); only the splits that the
 // row's visible keys reach were written, and only those are read, in order.
+// The sum is kept divided by its weights, so that it stays as large as a value.
 // ---------------------------------------------------------------------------
 // Lane s reads split s's log-sum-exp, so every weight is known after one load,
 // beside which the first COMBINE_BATCH partial rows are already on their way.
@@ -1587,10 +1588,13 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnPara
     const float top = fmaxf(warp_top(z), mx);
     const float f = mx == -INFINITY ? 0.f : expf(mx - top);
     // a split without a visible key weighs nothing; a NaN one makes the row NaN
-    const float w = z == -INFINITY ? 0.f : z != z ? z : expf(z - top);
-    wsum = wsum * f + warp_sum(w);
+    float w = z == -INFINITY ? 0.f : z != z ? z : expf(z - top);
+    const float before = wsum * f;
+    wsum = before + warp_sum(w);
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    w *= inv;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] *= f;
+    for (int e = 0; e < PER; ++e) acc[e] *= before * inv;
     mx = top;
     for (int k0 = 0; k0 < here; k0 += COMBINE_BATCH) {
       if (k0 > 0) load(k0);
@@ -1604,12 +1608,11 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(const AttnPara
       }
     }
   }
-  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   __nv_bfloat16* out = p.out + static_cast<size_t>(s.t0 + tok) * p.ldo +
                        static_cast<size_t>(h) * HD + lane * PER;
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e], acc[e + 1]);
   if (p.lse && lane == 0) p.lse[row] = wsum == 0.f ? -INFINITY : mx + logf(wsum);
 }
 

@@ -262,3 +262,19 @@ def test_large_weights_under_small_value_scales(kind, low):
         block[..., 0][nan] = 0x7F
         case.cache["k"][pages] = block
     check_attention(case, True, scale=60.0 / 28.0)
+
+
+def check_equal_values(kind, code, exp, value):
+    """Every value is the same, and so is every mean of them, exactly."""
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    case = Case(lengths, hkv, group, 64, 32, seed=87, exp_range=(121, 122))
+    case.cache["v"][:] = code
+    case.cache["v_exp"][:] = exp
+    out = check_attention(case, True)
+    assert (out.double() == value).all()
+
+
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
+def test_largest_finite_values(kind):
+    check_equal_values(kind, 0x38, 254, 2.0 ** 127)
+    check_equal_values(kind, 0xFE, 245, -448 * 2.0 ** 118)
