@@ -846,7 +846,10 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) emax = max(emax, s_emax[i]);
       // probabilities carry 2^P_SHIFT in O and in l alike; V carries 2^(V_SHIFT - emax)
-      const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(emax - 127 - V_SHIFT)) / l;
+      const int e_out = emax - 127 - V_SHIFT;
+      const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(max(e_out, -64))) / l;
+      // what a very small scale lacks, so that the quotient keeps its bits
+      const float rest = exp2f(static_cast<float>(min(e_out + 64, 0)));
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < HD / 64; ++c) {
@@ -857,9 +860,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const uint32_t* x = &o[v >> 3][(v & 7) * 4];
-          reinterpret_cast<float4*>(stage + r * HD)[(c * 16 + v) ^ (r & 7)] =
-              make_float4(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv,
-                          __uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
+          float4 y = make_float4(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv,
+                                 __uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
+          if (e_out < -64) {
+            y.x *= rest;
+            y.y *= rest;
+            y.z *= rest;
+            y.w *= rest;
+          }
+          reinterpret_cast<float4*>(stage + r * HD)[(c * 16 + v) ^ (r & 7)] = y;
         }
       }
       if (qrow < rows) {

@@ -178,7 +178,7 @@ def test_value_scales_at_the_ends(kind, exp):
     check_attention(case, True)
 
 
-@pytest.mark.parametrize("kind", [*NARROW])
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
 @pytest.mark.parametrize("exp", [1, 2])
 def test_value_scales_at_the_lower_end(kind, exp):
     """Results of 2^-126 and less: bf16 values lie 2^-133 apart there, so that their rounding is off
@@ -278,3 +278,10 @@ def check_equal_values(kind, code, exp, value):
 def test_largest_finite_values(kind):
     check_equal_values(kind, 0x38, 254, 2.0 ** 127)
     check_equal_values(kind, 0xFE, 245, -448 * 2.0 ** 118)
+
+
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
+def test_smallest_value_scales(kind):
+    check_equal_values(kind, 0x7E, 1, 448 * 2.0 ** -126)
+    check_equal_values(kind, 0xFE, 20, -448 * 2.0 ** -107)
+    check_equal_values(kind, 0x7E, 63, 448 * 2.0 ** -64)
