@@ -124,6 +124,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 struct AttnParams {
   Batch bt;
   int Hq, Hkv, group, causal;
@@ -728,9 +735,12 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     // keys [0, open_keys) are visible to every row of the CTA
     const int open_keys = p.causal ? s.c0 + token_of(p, first) + 1 : total;
     for (int j = 0; j < n && ok; ++j) {
-      float scg[8];  // row factor times the page scale, per 16 columns
+      // row factor times the page scale, per 16 columns; never zero, which a
+      // masked score of -infinity must not meet
+      float scg[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) scg[q] = sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)];
+      for (int q = 0; q < 8; ++q)
+        scg[q] = max_nan(sc * sKf[(j << log_ppt) + ((q * 16) >> bt.log_page)], FLT_MIN);
       if (!__all_sync(0xffffffffu, mbar_wait(&s_full[X], j & 1, abort_flag, 0x551))) {
         ok = false;
         break;

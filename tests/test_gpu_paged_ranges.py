@@ -169,6 +169,19 @@ def test_small_weights_beside_a_sink_many_rows(kind, bits):
 
 
 @pytest.mark.parametrize("kind", [*NARROW, *WIDE])
+@pytest.mark.parametrize("causal", [False, True])
+def test_zero_and_tiny_query_rows(kind, causal):
+    """Scores that underflow to zero: the rows are plain means of what they see."""
+    lengths, hkv, group = {**NARROW, **WIDE}[kind]
+    for k_exp, scale in ((79, None), (60, None), (1, None), (87, 1e-4), (121, 1e-38)):
+        case = Case(lengths, hkv, group, 64, 32, seed=82, exp_range=(121, 122))
+        case.cache["k_exp"][:] = k_exp
+        case.q[::3] = 0.0
+        case.q[1::3] *= 2.0 ** -120
+        check_attention(case, causal, scale=scale)
+
+
+@pytest.mark.parametrize("kind", [*NARROW, *WIDE])
 @pytest.mark.parametrize("exp", [30, 87, 200, 227, 253, 254])
 def test_value_scales_at_the_ends(kind, exp):
     lengths, hkv, group = {**NARROW, **WIDE}[kind]
