@@ -9,8 +9,9 @@
 // power-of-two scale 2^e:
 //   e    = the smallest integer with max |x| <= 448 2^e over the page's new
 //          rows (finite values only), clamped to [-40, 100];
-//   kept = rows of the page below cache_len[b]: e is at least their old scale,
-//          and if it grew their codes are rounded again to the new one;
+//   kept = rows of the page below cache_len[b]: e is at least their old scale
+//          (even one above 100, in a page of another origin), and if it grew
+//          their codes are rounded again to the new one;
 //   code = e4m3(x 2^-e), nearest, ties to even, saturating.
 // A power of two makes both the scaling and a later attention's dequantisation
 // exact, and a re-rounding loses bits only where codes turn subnormal.
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 3) append_kernel(const AppendP
   uint8_t* dst = (is_v ? p.v_pages : p.k_pages) + (head << bt.log_page) * HD;
   uint8_t* exp_at = (is_v ? p.v_exp : p.k_exp) + head;
   const bool keeps = r_beg > 0;  // rows of earlier appends stay in this page
-  const int e_old = keeps ? min(static_cast<int>(*exp_at) - 127, SCALE_MAX) : SCALE_MIN;
+  const int e_old = keeps ? static_cast<int>(*exp_at) - 127 : SCALE_MIN;
 
   uint4 ra[ROWS], rb[ROWS];
 #pragma unroll
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 3) append_kernel(const AppendP
   }
   if (!live) return;
   const int e = max(scale_exponent(amax), e_old);
-  const float f = pow2(-e);
+  const float f = e < 127 ? pow2(-e) : __uint_as_float(0x800000u >> (e - 126));  // subnormal
 #pragma unroll
   for (int u = 0; u < ROWS; ++u) {
     const int r = row0 + u * row_step;

@@ -321,10 +321,10 @@ int dg_canvas_attn_e4m3(const uint8_t* q, int ldq, const float* q_scale, const u
  * Scale of a page and kv head: 2^e with e the smallest integer for which the
  * page's new rows satisfy max |x| <= 448 2^e (infinities and NaN left out),
  * within [-40, 100]; where rows of earlier appends stay in the page (positions
- * below cache_len), e is at least their old scale's, and their codes are
- * rounded again (nearest, ties to even) if it grew.  Codes: x / 2^e, nearest e4m3
- * value, ties to even, saturating at 448; NaN stays NaN.  Rows of a page
- * behind the last new one are left as they are.
+ * below cache_len), e is at least their old scale's, whatever that is, and their
+ * codes are rounded again (nearest, ties to even) if it grew.  Codes: x / 2^e,
+ * nearest e4m3 value, ties to even, saturating at 448; NaN stays NaN.  Rows of a
+ * page behind the last new one are left as they are.
  * A page that is written must belong to one sequence (pages that are full and
  * only read may be shared); page ids that appear twice among the written ones
  * leave that page's contents undefined.  Needs no workspace.

@@ -11,7 +11,7 @@ import torch
 import test_gpu_paged as base
 from oracle import paged
 from paged_cases import Case
-from test_gpu_paged import dg
+from test_gpu_paged import check_append, dg
 
 pytestmark = pytest.mark.gpu
 
@@ -298,3 +298,15 @@ def test_smallest_value_scales(kind):
     check_equal_values(kind, 0x7E, 1, 448 * 2.0 ** -126)
     check_equal_values(kind, 0xFE, 20, -448 * 2.0 ** -107)
     check_equal_values(kind, 0x7E, 63, 448 * 2.0 ** -64)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("page", [16, 128])
+def test_append_keeps_scales_above_its_own_largest(hd, page):
+    """Pages of another origin may hold exponents up to 254: kept rows keep their values."""
+    for lo, hi in ((226, 232), (240, 255)):
+        case = Case([(1, page - 1), (2, 2 * page - 3), (40, page + 1), (page, 5)], 2, 1, hd, page,
+                    seed=86, exp_range=(lo, hi))
+        case.k *= 2.0 ** 100
+        case.v *= 2.0 ** 118
+        check_append(case, 0)
