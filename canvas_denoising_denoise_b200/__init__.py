@@ -299,7 +299,10 @@ def kv_block_commit(k_blk, v_blk, k_cache, v_cache, cache_len, *, n_kv_heads, he
 
 class PagedCache:
     """One layer's paged e4m3 KV cache: k_pages, v_pages uint8 [n_pages, Hkv, page, hd] (e4m3
-    codes) and k_exp, v_exp uint8 [n_pages, Hkv] (a page's scale is 2^(exp - 127))."""
+    codes) and k_exp, v_exp uint8 [n_pages, Hkv] (a page's scale is 2^(exp - 127)).
+
+    The four tensors are the cache's for its life: make another PagedCache for other ones.
+    """
 
     def __init__(self, k_pages, v_pages, k_exp, v_exp):
         tensors = (k_pages, v_pages, k_exp, v_exp)
@@ -311,10 +314,24 @@ class PagedCache:
         if any(t.device != k_pages.device for t in tensors):
             raise ValueError("codes and exponents must be on one device")
         _need_contig(*tensors)
-        self.k_pages, self.v_pages, self.k_exp, self.v_exp = tensors
+        self._tensors = tensors
+        self._sizes = (k_pages.numel(), k_exp.numel())
         self.n_pages, self.n_kv_heads, self.page, self.head_dim = k_pages.shape
         self.device_index = k_pages.get_device()
-        self.pointers = tuple(t.data_ptr() for t in tensors)  # the tensors above keep them valid
+
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    k_exp = property(lambda self: self._tensors[2])
+    v_exp = property(lambda self: self._tensors[3])
+
+    @property
+    def pointers(self):
+        """Device pointers of the four tensors as they are now (set_() and the like move them)."""
+        k, v, ke, ve = self._tensors
+        codes, exps = self._sizes
+        if k.numel() != codes or v.numel() != codes or ke.numel() != exps or ve.numel() != exps:
+            raise ValueError("the cache's tensors were resized")
+        return k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr()
 
     @classmethod
     def zeros(cls, n_pages, n_kv_heads, page, head_dim, device="cuda"):
