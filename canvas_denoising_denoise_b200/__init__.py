@@ -478,7 +478,11 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
         buf = ws.buf
         status = call(buf.data_ptr(), buf.numel()) if buf is not None else call(None, 0)
         if status == _lib.DG_ERR_WORKSPACE_TOO_SMALL:
-            status = call(*ws.args(need()))
+            with torch.cuda.stream(stream):  # a no-op for None
+                if buf is not None:  # earlier calls of this stream may still use it
+                    buf.record_stream(torch.cuda.current_stream())
+                buf = ws.get(need())
+            status = call(buf.data_ptr(), buf.numel())
     else:
         wn, wp = need(), None
         if wn:

@@ -1,8 +1,12 @@
-"""The Python side of the paged calls on the CPU: whose memory they hand to the library."""
+"""The Python side of the paged calls on the CPU: whose memory they hand to the library, and
+on which stream they take it.  No kernel runs."""
+import contextlib
+
 import pytest
 import torch
 
 import canvas_denoising_denoise_b200 as dg
+from canvas_denoising_denoise_b200 import _lib
 
 
 def tensors(n_pages):
@@ -29,3 +33,73 @@ def test_a_caches_pointers_follow_its_tensors(at):
     parts[at].resize_(1 << 20)
     with pytest.raises(ValueError):
         cache.pointers
+
+
+class Library:
+    """Answers as the library does to a workspace that is too small for `need` bytes."""
+
+    def __init__(self, need, log):
+        self.need, self.log = need, log
+
+    def dg_paged_attn_workspace_bytes(self, *sizes):
+        return self.need
+
+    def dg_paged_attn_e4m3(self, *args):
+        pointer, size = args[-3:-1]
+        self.log.append(("call", size))
+        return 4 if not pointer or size < self.need else 0
+
+
+def test_a_workspace_grows_on_the_calls_stream(monkeypatch):
+    """Its memory belongs to the stream that the kernels run on, and the memory that it replaces is
+    kept from other use until that stream has passed it."""
+    log = []
+
+    class Stream:
+        cuda_stream = 7
+
+    class Buffer:  # the workspace's earlier memory
+        def get_device(self):
+            return -1
+
+        def data_ptr(self):
+            return 4096
+
+        def numel(self):
+            return 300
+
+        def record_stream(self, stream):
+            log.append(("keep for", stream))
+
+    @contextlib.contextmanager
+    def on(stream):
+        log.append(("enter", stream))
+        yield
+        log.append(("leave", stream))
+
+    class Workspace(dg.Workspace):
+        def get(self, nbytes):
+            log.append(("allocate", nbytes))
+            return super().get(nbytes)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(dg, "_ptr", lambda t: t.data_ptr())
+    monkeypatch.setattr(dg, "_paged_batch", lambda *a: (1, 2, 3, 1, 4, -1))
+    monkeypatch.setattr(_lib, "load", lambda: Library(1000, log))
+    cache = dg.PagedCache(*tensors(4))
+    q = torch.zeros((1, 128), dtype=torch.bfloat16)
+    side, ws = Stream(), Workspace("cpu")
+    ws.buf = Buffer()
+
+    def call():
+        dg.paged_attn_e4m3(q, cache, None, None, None, 1, 64, q, n_q_heads=2, ws=ws, stream=side)
+
+    call()
+    assert ("keep for", "current") in log  # the current stream within the block: the call's
+    assert [e for e in log if e[0] != "keep for"] == [
+        ("call", 300), ("enter", side), ("allocate", 1000), ("leave", side), ("call", 1000)]
+    assert log.index(("enter", side)) < log.index(("keep for", "current")) < log.index(("allocate", 1000))
+    log.clear()
+    call()  # large enough now: one call, nothing else
+    assert log == [("call", 1000)]
