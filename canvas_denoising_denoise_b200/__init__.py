@@ -476,12 +476,16 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
     if ws is not None:
         # a workspace that has grown to the shape once needs no query
         buf = ws.buf
+        if buf is not None and buf.get_device() != dev:
+            raise ValueError("ws must be on the cache's device")
         status = call(buf.data_ptr(), buf.numel()) if buf is not None else call(None, 0)
         if status == _lib.DG_ERR_WORKSPACE_TOO_SMALL:
             with torch.cuda.stream(stream):  # a no-op for None
                 if buf is not None:  # earlier calls of this stream may still use it
                     buf.record_stream(torch.cuda.current_stream())
                 buf = ws.get(need())
+            if buf.get_device() != dev:
+                raise ValueError("ws must be on the cache's device")
             status = call(buf.data_ptr(), buf.numel())
     else:
         wn, wp = need(), None

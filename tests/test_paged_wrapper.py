@@ -103,3 +103,39 @@ def test_a_workspace_grows_on_the_calls_stream(monkeypatch):
     log.clear()
     call()  # large enough now: one call, nothing else
     assert log == [("call", 1000)]
+
+
+def no_gpu(monkeypatch, library):
+    """The calls' own checks and marshalling, on CPU tensors."""
+    monkeypatch.setattr(dg, "_paged_batch", lambda *a: (1, 2, 3, 1, 4, -1))
+    monkeypatch.setattr(dg, "_raw_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(_lib, "load", lambda: library)
+    return dg.PagedCache(*tensors(4)), torch.zeros((3, 128), dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("grown", [False, True])
+def test_a_workspace_on_another_device_is_refused(monkeypatch, grown):
+    log = []
+    cache, q = no_gpu(monkeypatch, Library(1000, log))
+
+    class Elsewhere:
+        def get_device(self):
+            return 1
+
+        def data_ptr(self):
+            return 4096
+
+        def numel(self):
+            return 2000
+
+    class Workspace(dg.Workspace):
+        def get(self, nbytes):
+            self.buf = Elsewhere()
+            return self.buf
+
+    ws = Workspace("cuda:1")
+    if grown:
+        ws.get(2000)
+    with pytest.raises(ValueError, match="device"):
+        dg.paged_attn_e4m3(q, cache, None, None, None, 1, 64, q, n_q_heads=2, ws=ws)
+    assert all(size == 0 for _, size in log)  # its pointer was not handed over
