@@ -408,6 +408,7 @@ def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, ro
     T, Hkv, hd = k.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return
+    max_new = min(max_new, T)  # (past 32 bits it would wrap around)
     ldkv, _, kp = _rows(k, "k", dev, T, Hkv * hd)
     ldv, _, vp = _rows(v, "v", dev, T, Hkv * hd)
     if ldv != ldkv:
@@ -451,6 +452,8 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
     T, Hkv, hd = q.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return out
+    # (bounds past these say nothing more, and past 32 bits would wrap around)
+    max_new, max_prefix = min(max_new, T), min(max_prefix, max_pages * cache.page)
     ldq, _, qp = _rows(q, "q", dev, T, n_q_heads * hd)
     ldo, _, op = _rows(out, "out", dev, T, n_q_heads * hd)
     zp = None

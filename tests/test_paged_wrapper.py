@@ -139,3 +139,31 @@ def test_a_workspace_on_another_device_is_refused(monkeypatch, grown):
     with pytest.raises(ValueError, match="device"):
         dg.paged_attn_e4m3(q, cache, None, None, None, 1, 64, q, n_q_heads=2, ws=ws)
     assert all(size == 0 for _, size in log)  # its pointer was not handed over
+
+
+class Recorder:
+    def __init__(self):
+        self.args = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.args[name] = args
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("bound", [3, 64, (1 << 31) - 1, 1 << 32, (1 << 40) + 3])
+def test_bounds_past_32_bits_stay_bounds(monkeypatch, bound):
+    """A bound on the new rows counts up to T, one on the cached rows up to the table's positions: a
+    larger one must not wrap around (to no rows, say, and a call that does nothing)."""
+    library = Recorder()
+    cache, q = no_gpu(monkeypatch, library)
+    kv = torch.zeros((3, 128), dtype=torch.bfloat16)
+    dg.kv_append_e4m3(kv, kv, cache, None, None, None, bound)
+    dg.paged_attn_e4m3(q, cache, None, None, None, bound, bound, q, n_q_heads=2)
+    append, attn = library.args["dg_kv_append_e4m3"], library.args["dg_paged_attn_e4m3"]
+    query = library.args["dg_paged_attn_workspace_bytes"]
+    positions = 4 * 16  # of the table that no_gpu stands for
+    assert append[-6] == 3  # max_new
+    assert attn[12:14] == (3, min(bound, positions))
+    assert query[-2:] == (3, min(bound, positions))
