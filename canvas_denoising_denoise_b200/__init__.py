@@ -315,7 +315,9 @@ class PagedCache:
             raise ValueError("codes and exponents must be on one device")
         _need_contig(*tensors)
         self._tensors = tensors
-        self._sizes = (k_pages.numel(), k_exp.numel())
+        self._sizes = tuple(t.numel() for t in tensors)
+        self._data_ptrs = tuple(t.data_ptr for t in tensors)
+        self._checked = tuple(t.data_ptr() for t in tensors)
         self.n_pages, self.n_kv_heads, self.page, self.head_dim = k_pages.shape
         self.device_index = k_pages.get_device()
 
@@ -327,11 +329,13 @@ class PagedCache:
     @property
     def pointers(self):
         """Device pointers of the four tensors as they are now (set_() and the like move them)."""
-        k, v, ke, ve = self._tensors
-        codes, exps = self._sizes
-        if k.numel() != codes or v.numel() != codes or ke.numel() != exps or ve.numel() != exps:
-            raise ValueError("the cache's tensors were resized")
-        return k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr()
+        k, v, ke, ve = self._data_ptrs
+        at = (k(), v(), ke(), ve())
+        if at != self._checked:  # memory of another size lies elsewhere
+            if tuple(t.numel() for t in self._tensors) != self._sizes:
+                raise ValueError("the cache's tensors were resized")
+            self._checked = at
+        return at
 
     @classmethod
     def zeros(cls, n_pages, n_kv_heads, page, head_dim, device="cuda"):
@@ -408,7 +412,8 @@ def kv_append_e4m3(k, v, cache, page_table, tok_start, cache_len, max_new, *, ro
     T, Hkv, hd = k.shape[0], cache.n_kv_heads, cache.head_dim
     if T == 0:
         return
-    max_new = min(max_new, T)  # (past 32 bits it would wrap around)
+    if max_new > T:  # (past 32 bits it would wrap around)
+        max_new = T
     ldkv, _, kp = _rows(k, "k", dev, T, Hkv * hd)
     ldv, _, vp = _rows(v, "v", dev, T, Hkv * hd)
     if ldv != ldkv:
@@ -453,7 +458,10 @@ def paged_attn_e4m3(q, cache, page_table, tok_start, cache_len, max_new, max_pre
     if T == 0:
         return out
     # (bounds past these say nothing more, and past 32 bits would wrap around)
-    max_new, max_prefix = min(max_new, T), min(max_prefix, max_pages * cache.page)
+    if max_new > T:
+        max_new = T
+    if max_prefix > max_pages * cache.page:
+        max_prefix = max_pages * cache.page
     ldq, _, qp = _rows(q, "q", dev, T, n_q_heads * hd)
     ldo, _, op = _rows(out, "out", dev, T, n_q_heads * hd)
     zp = None
