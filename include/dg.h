@@ -350,7 +350,7 @@ int dg_kv_append_e4m3(const void* k, const void* v, int ldkv, const void* q, int
  * Queries enter the product at bf16 precision (a row's elements below 2^-10 of
  * its largest to 2^-18 of that), key and value codes as they are cached; a
  * probability is rounded to 2^-11 of itself, and where that is more, it times
- * its page's value scale to 2^-29 of the largest probability times the largest
+ * its page's value scale to 2^-27 of the largest probability times the largest
  * value scale of its sequence's pages; sums and softmax statistics are fp32.
  * Exponents must lie in [1, 254], scaled scores within +-2^23.  Positions from
  * cache_len[b] + n_b on may hold any codes, NaN among them.  A NaN or an

@@ -261,6 +261,15 @@ def test_value_scales_far_apart_in_blocks_of_pages(kind):
 
 
 @pytest.mark.parametrize("kind", [k for k in (*NARROW, *WIDE) if k != "one key"])
+@pytest.mark.parametrize("exps", [(70, 99, 102, 60), (70, 72, 75, 71), (60, 90, 120, 121), (40, 41, 43, 46),
+                                  (127, 129, 132, 250)])
+def test_value_scales_that_rise_in_steps(kind, exps):
+    """A tile of each scale in turn: small steps, a large one, a small one behind it."""
+    check_attention(spread_case(kind, tuple(np.repeat(exps, 8))), True)
+    check_attention(spread_case(kind, tuple(np.repeat(exps, 2)), page=64), True)
+
+
+@pytest.mark.parametrize("kind", [k for k in (*NARROW, *WIDE) if k != "one key"])
 @pytest.mark.parametrize("low", [0, 1])
 def test_large_weights_under_small_value_scales(kind, low):
     """The keys of pages with the small scale stand 60 nats above the others (log-sum-exp tells)."""
