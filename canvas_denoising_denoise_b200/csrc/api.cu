@@ -694,7 +694,9 @@ int launch_append(const dg::paged::AppendParams& p, dim3 grid, cudaStream_t s) {
 // Execution plan of the paged attention, from the shape's bounds alone (so a
 // shape always gives the same bits).  Up to 32 packed rows per kv head run with
 // keys along the tensor core's M (narrow_kernel, `rows` = 16 or 32), more with
-// 256-row query blocks (wide_kernel, rows = 0).
+// 256-row query blocks (wide_kernel, rows = 0).  16 sequences of 8193 keys, 8 kv
+// heads of 128, narrow against wide: 93 / 118 us at 20 rows, 108 / 118 at 32
+// (2049 keys: 35 / 38 and 40 / 38; one sequence of 4097: 17.5 / 16 and 22 / 17).
 struct PagedPlan {
   int rows, n_pairs, tiles_per_split, n_splits;
   bool merge;   // the splits of a unit run as one cluster and merge in shared memory
@@ -739,11 +741,12 @@ PagedPlan plan_paged(int B, int Hq, int Hkv, int hd, int max_new, long long max_
     pl.rows = rows <= 16 ? 16 : 32;
     pl.n_pairs = 1;
     units = (long long)B * Hkv;
-    slots = kNumSMs * (pl.rows == 32 ? 1 : hd == 128 ? 2 : 3);
+    slots = kNumSMs * (pl.rows == 32 ? 1 : 2);
     splits = best_splits(units, tiles, slots, {800.0, 3000.0, 3000.0, split_ns}, kNumSMs * 2);
-    // Few units: as many splits as a cluster holds, merged by it (13.4 us, one
-    // token over 4096 keys and 8 kv heads; 14.5 with a second launch), unless
-    // they would be long or the clusters more than the GPU places at once.
+    // Few units: as many splits as a cluster holds, merged by it, unless they
+    // would be long or the clusters more than the GPU places at once.  One token,
+    // 8 kv heads of 128, the cluster against more splits and a second launch:
+    // 9.9 / 12.4 us at 4097 keys, 13.6 / 13.7 at 8193, 16.1 / 14.7 at 12289.
     if (tiles > 1 && units * MAX_CLUSTER <= kNumSMs && cdiv(tiles, MAX_CLUSTER) <= 8) {
       splits = std::min(splits, MAX_CLUSTER);
       pl.merge = true;

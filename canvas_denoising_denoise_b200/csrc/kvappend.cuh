@@ -25,8 +25,9 @@
 //
 // Bound by HBM for long prompts: four of up to 4096 rows (8 kv and 16 query
 // heads of 128) in 32 us, 4.8 TB/s, 73% of the measured copy rate, with a third
-// of the SM's warps resident (80 registers: the rows are held in fp32) and 44%
-// of its issue slots taken by conversions and rotation.  Canvases and single
+// of the SM's warps resident (three CTAs: 80 registers with the rows held in
+// fp32, and at hd 128 still 104 bytes of spill loads) and 45% of its issue
+// slots taken by conversions and rotation.  Canvases and single
 // tokens are launch and latency: 3 to 7 us.
 #pragma once
 

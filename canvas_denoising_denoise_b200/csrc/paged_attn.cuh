@@ -12,9 +12,10 @@
 // split into two e4m3 values hi + lo (4 + 4 significant bits: exact for
 // elements down to 2^-10 of the row's largest, below that to 2^-18 of it), and
 // both halves are multiplied by the same key codes with fp32 accumulation.
-// V codes become f16 times a power of two relative to the CTA's largest page
-// scale (exact to 2^-31 of the largest value), and the probabilities f16
-// (2^-11 relative): an 8-bit probability would lose 2^-4.
+// The probabilities are f16 (2^-11 of themselves): an 8-bit one would lose 2^-4.
+// With many rows V codes become f16 times a power of two relative to the CTA's
+// largest page scale (exactly for scales down to 2^-22 of that, below to 2^-32
+// of it), and weights below 2^-21 of the largest are held to 2^-32 of it.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -380,8 +381,10 @@ __device__ __forceinline__ int nth_longest(const Batch& bt, int want, int* scrat
 // starts while the second half is still being formed.
 // Measured: 32 heads x 256 rows over 32768 + 256 keys (hd 128) in 150 us with
 // the merge, 0.92 PFLOP/s, 57% of the measured bf16 rate; a 4096-row causal
-// prompt behind 1031 rows in 120 us, 54%.  Where the key range is short the
-// set-up and epilogue of a CTA (8 us) weigh as much as its tiles.
+// prompt behind 1031 rows in 120 us, 54%.  With hd 64 a tile has half the FLOP
+// and the same softmax: 133 and 110 us.  Where the key range is short the
+// set-up and epilogue of a CTA (8 us) weigh as much as its tiles.  16 bytes of
+// a thread's state are spilled.
 constexpr int WIDE_THREADS = 512;
 constexpr float P_SHIFT = 7.f;  // probabilities are held as 2^(s - m + 7): at most 2^15 in f16
 constexpr int V_SHIFT = 7;      // V codes as code 2^(ev - emax + 7): at most 57344 in f16
@@ -967,12 +970,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 // 2^-27 of the largest probability at the largest scale.  The largest weight's
 // part of the sum lies between 2^2 and 2^56, and weights down to 2^-80 of it
 // are not lost.
-// Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 165 us, 6.5 TB/s,
-// the measured copy rate; of 20 to 100% of that length 107 us, 92%; one
-// sequence of 4097 keys 9 us, which is launch, first loads and the merge.  With
-// hd 64 a tile has half the bytes and takes as long (its chain of scores,
-// barrier, P and P V is the same): 150 us for the 64 of 8193 where the bytes
-// need 82.
+// Measured: 64 sequences of 8193 keys, 32 / 8 heads, hd 128: 164 us, 6.5 TB/s,
+// the measured copy rate; of 20 to 100% of that length 109 us, 90%; one
+// sequence of 4097 keys 9.9 us, which is launch, first loads and the merge.
+// Otherwise a tile's chain of scores, barrier, P and P V bounds it.  With hd 64
+// a tile has half the bytes and the same chain: 136 us for the 64 of 8193,
+// where the bytes need 82.  With 17 to 32 rows a thread holds 32 scores and
+// sums (254 registers, one CTA an SM): 16 sequences of 8193 keys in 93 us at 20
+// rows and 108 at 32, where the bytes need 41.
+// Two CTAs an SM for NR = 16: 146 registers, no spills.  With hd 64 shared
+// memory would hold three, at 96 registers and 340 bytes of spill loads: 162 us
+// instead of 136, 300 sequences of 301 keys 65 instead of 70.
 //
 // Warps: 0 = TMA producer, 1 = TMEM owner + MMA issuer, 2..5 = softmax (thread
 // = key; at the end thread = element of the head).
@@ -1030,7 +1038,7 @@ __device__ __forceinline__ int p_swz(int r, int c) {
 }
 
 template <int HD, int NR>
-__global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : HD == 128 ? 2 : 3)
+__global__ void __launch_bounds__(NARROW_THREADS, NR == 32 ? 1 : 2)
     narrow_kernel(const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p) {
   using CF = Narrow<HD, NR>;
