@@ -321,6 +321,9 @@ class PagedCache:
         self.n_pages, self.n_kv_heads, self.page, self.head_dim = k_pages.shape
         self.device_index = k_pages.get_device()
 
+    def __reduce__(self):  # copies are made of the tensors, not of what points into them
+        return type(self), self._tensors
+
     k_pages = property(lambda self: self._tensors[0])
     v_pages = property(lambda self: self._tensors[1])
     k_exp = property(lambda self: self._tensors[2])

@@ -1,6 +1,8 @@
 """The Python side of the paged calls on the CPU: whose memory they hand to the library, and
 on which stream they take it.  No kernel runs."""
 import contextlib
+import copy
+import pickle
 
 import pytest
 import torch
@@ -33,6 +35,16 @@ def test_a_caches_pointers_follow_its_tensors(at):
     parts[at].resize_(1 << 20)
     with pytest.raises(ValueError):
         cache.pointers
+
+
+@pytest.mark.parametrize("how", [copy.deepcopy, lambda c: pickle.loads(pickle.dumps(c))])
+def test_a_copied_cache_has_its_own_memory(how):
+    cache = dg.PagedCache(*tensors(4))
+    cache.k_pages.fill_(3)
+    other = how(cache)
+    own = tuple(t.data_ptr() for t in (other.k_pages, other.v_pages, other.k_exp, other.v_exp))
+    assert other.pointers == own and not set(own) & set(cache.pointers)
+    assert other.n_pages == 4 and torch.equal(other.k_pages, cache.k_pages)
 
 
 class Library:
